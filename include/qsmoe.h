@@ -61,13 +61,24 @@ typedef enum {
 typedef enum { MOE_FMT_AFFINE = 0, MOE_FMT_MXFP4 = 1, MOE_FMT_MXFP8 = 2 } moe_format;
 typedef enum { MOE_ROUTE_TOPK = 0, MOE_ROUTE_HASH = 1 } moe_route_mode;
 typedef enum { MOE_OUT_BF16 = 0, MOE_OUT_F32 = 1 } moe_out_dtype;
+/* Element types of the plain matrices of the block-scaled and grouped products
+ * (the first two as in moe_out_dtype). */
+typedef enum { MOE_DT_BF16 = 0, MOE_DT_F32 = 1, MOE_DT_F16 = 2 } moe_dtype;
+/* How the rows of a matrix stand to the T*k assignments that moe_permute
+ * bucketed; bucket position p is assignment perm[p].
+ *   MOE_ROWS_BUCKET  [T*k] rows, row p belongs to position p (perm not read)
+ *   MOE_ROWS_TOKEN   [T] rows, position p reads row perm[p] / k
+ *   MOE_ROWS_SLOT    [T*k] rows, row perm[p] belongs to position p */
+typedef enum { MOE_ROWS_BUCKET = 0, MOE_ROWS_TOKEN = 1, MOE_ROWS_SLOT = 2 } moe_rows;
 
 /* Device error bits ORed into the workspace's error word. */
 #define MOE_DEVERR_TOKEN_ID 1  /* token id outside [0, vocab)                  */
 #define MOE_DEVERR_HASH_ID 2   /* tid2eid entry outside [0, E)                  */
 #define MOE_DEVERR_EXPERT_ID 4 /* top-k id passed to moe_permute outside [0, E) */
 #define MOE_DEVERR_QUANT_INPUT 8 /* moe_quantize_affine: a NaN/inf weight, or a group's
-                                    scale or bias beyond fp16 (outputs unspecified) */
+                                    scale or bias beyond fp16 (outputs unspecified);
+                                    moe_quantize_block: a NaN/inf input */
+#define MOE_DEVERR_ROW_INDEX 16 /* a perm entry of a grouped product outside its rows */
 
 /*
  * One stacked quantised projection: num_experts matrices of [rows][cols].
@@ -373,6 +384,101 @@ moe_status moe_quantize_affine(const uint16_t* w_bf16, int64_t rows, int32_t col
  */
 moe_status moe_mhc_sinkhorn(const float* logits, int64_t T, int32_t n, int32_t iters, float eps, float* out,
                             hipStream_t stream);
+
+/*
+ * Block-scaled FP8 (ops beside the layer). A matrix is held as OCP E4M3 codes
+ * (one byte per element, as in MOE_FMT_MXFP8) with one fp32 scale per block of
+ * 128 columns and 1 or 128 rows; an element stands for code * scale.
+ * Activations use 1 x 128 blocks, weights 128 x 128; blocks at the right and
+ * lower edge may be smaller.
+ *
+ * moe_quantize_block: x [matrices][rows][cols] -> codes of the same shape and
+ * scales [matrices][ceil(rows / block_rows)][ceil(cols / 128)]. Per block, in
+ * fp32 with IEEE rounding, amax the largest |x| of the block:
+ *     s = max(amax / 448, 2^-126),  code = e4m3_rne(x * (1 / s));
+ * with pow2 != 0 the quotient amax / 448 is first raised to the next power of
+ * two, which makes scaling and unscaling exact. A block that holds a NaN or an
+ * infinity gets the scale NaN and codes 0, and MOE_DEVERR_QUANT_INPUT is ORed
+ * into *err (err: device int32 or NULL); the other blocks are not affected.
+ * dtype: moe_dtype of x. block_rows in {1, 128}; cols % 16 == 0; x and codes
+ * 16-byte, scales and err 4-byte aligned. Nothing to do (MOE_OK, no launch)
+ * when a size is 0. Errors: INVALID_ARG (null, negative, dtype), UNSUPPORTED
+ * (block_rows, cols, more than 2^31 - 1 workgroups), ALIGNMENT, HIP.
+ */
+moe_status moe_quantize_block(const void* x, int32_t dtype, int64_t matrices, int64_t rows, int32_t cols,
+                              int32_t block_rows, int32_t pow2, uint8_t* codes, float* scales, int32_t* err,
+                              hipStream_t stream);
+
+/* moe_swiglu_quantize_block: the step between an expert's two products. gu
+ * [rows][2 * inner] holds gate in its first `inner` columns and up in the
+ * others; h = silu(gate) * up in fp32, quantised as moe_quantize_block does
+ * with block_rows = 1 (h itself is not rounded to 16 bits in between): codes
+ * [rows][inner], scales [rows][ceil(inner / 128)]. inner % 16 == 0; the rest
+ * as above (a block whose h holds a NaN or an infinity counts as such). */
+moe_status moe_swiglu_quantize_block(const void* gu, int32_t dtype, int64_t rows, int32_t inner, int32_t pow2,
+                                     uint8_t* codes, float* scales, int32_t* err, hipStream_t stream);
+
+/*
+ * moe_matmul_block: out[m][n] = sum_k a[m][k] * b[n][k] over the values the
+ * codes stand for; products and sums in fp32 (the 128 products of a block are
+ * summed before the two scales multiply the sum), one rounding to the output.
+ *   a [M][K] codes, a_scales [M][ceil(K / 128)]              (1 x 128)
+ *   b [N][K] codes, b_scales [ceil(N / 128)][ceil(K / 128)]  (128 x 128)
+ *   out [M][N], out_dtype MOE_DT_BF16, MOE_DT_F32 or MOE_DT_F16
+ * K % 16 == 0, N % 8 == 0, N and K <= 2^20; a, b and out 16-byte, scales 4-byte
+ * aligned. M, N or K of 0: MOE_OK (K == 0 writes zeros). Errors: INVALID_ARG,
+ * UNSUPPORTED, ALIGNMENT, HIP.
+ */
+moe_status moe_matmul_block(const uint8_t* a, const float* a_scales, const uint8_t* b, const float* b_scales,
+                            int32_t M, int32_t N, int32_t K, int32_t out_dtype, void* out, hipStream_t stream);
+
+/*
+ * Matrix products grouped by expert. offsets int32 [E+1] (device) and perm
+ * int32 [T*k] (device) are those of moe_permute: positions offsets[e] ..
+ * offsets[e+1] - 1 use expert e's weights. An expert may have no position;
+ * positions outside every bucket (before offsets[0], from offsets[E] on) are
+ * neither read nor written, so their output rows stay as they were. Offsets
+ * are clamped to [0, T*k], and buckets that do not ascend count as empty. A
+ * perm entry outside [0, T*k) sets MOE_DEVERR_ROW_INDEX in *err (device int32
+ * or NULL); row 0 is read in its place, and an output row that it would name
+ * is not written. perm may be NULL when no matrix is in token or slot order;
+ * it must not name an output row twice.
+ *
+ * moe_grouped_matmul_block: out[p][n] = sum_k a[p][k] * w[e(p)][n][k] over
+ * block-scaled FP8, as moe_matmul_block: a in a_order, w [E][N][K], w_scales
+ * [E][ceil(N / 128)][ceil(K / 128)], out in out_order (BUCKET or SLOT).
+ *
+ * moe_grouped_matmul: the same for 16-bit x and w [E][N][K] of one type
+ * (dtype MOE_DT_BF16 or MOE_DT_F16): out[p][n] = sum_k x[p][k] w[e][n][k], or
+ * with transposed != 0 out[p][k] = sum_n x[p][n] w[e][n][k] (x has N columns:
+ * the gradient in the rows). fp32 sums, one rounding to the output.
+ *
+ * moe_grouped_matmul_dw: the gradient in the weights, out[e][n][k] = sum over
+ * expert e's positions of dy[p][n] * x[p][k]; x in x_order, dy in dy_order
+ * (BUCKET or SLOT); out [E][N][K], zeros for an expert without a position.
+ * fp32 sums in a fixed order (no atomics).
+ *
+ * T, k, E >= 1 sized as in moe_permute but for k, which only has to be >= 1
+ * (T*k < 2^31, E <= 1024). FP8: K % 16 == 0, N % 8 == 0; 16-bit: K % 8 == 0,
+ * N % 8 == 0; N and K <= 2^20. out_dtype MOE_DT_BF16, MOE_DT_F32 or
+ * MOE_DT_F16. Matrices 16-byte, offsets, perm, scales and err 4-byte aligned.
+ * T == 0, or nothing to write: MOE_OK without a launch, but dw still writes
+ * its zeros; a contraction of length 0 gives zeros. No workspace. Errors:
+ * INVALID_ARG, UNSUPPORTED, ALIGNMENT, HIP.
+ */
+moe_status moe_grouped_matmul_block(const uint8_t* a, const float* a_scales, const uint8_t* w, const float* w_scales,
+                                    int32_t T, int32_t k, int32_t N, int32_t K, int32_t E, const int32_t* offsets,
+                                    const int32_t* perm, int32_t a_order, int32_t out_order, int32_t out_dtype,
+                                    void* out, int32_t* err, hipStream_t stream);
+
+moe_status moe_grouped_matmul(const void* x, const void* w, int32_t dtype, int32_t T, int32_t k, int32_t N, int32_t K,
+                              int32_t E, const int32_t* offsets, const int32_t* perm, int32_t x_order,
+                              int32_t out_order, int32_t transposed, int32_t out_dtype, void* out, int32_t* err,
+                              hipStream_t stream);
+
+moe_status moe_grouped_matmul_dw(const void* x, const void* dy, int32_t dtype, int32_t T, int32_t k, int32_t N,
+                                 int32_t K, int32_t E, const int32_t* offsets, const int32_t* perm, int32_t x_order,
+                                 int32_t dy_order, int32_t out_dtype, void* out, int32_t* err, hipStream_t stream);
 
 const char* moe_status_string(moe_status status);
 

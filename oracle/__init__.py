@@ -9,3 +9,4 @@ Every function is plain numpy in float64, written for a reader to check by eye
 against the pages it cites; see ``oracle.moe``.
 """
 from .moe import *  # noqa: F401,F403
+from .products import *  # noqa: F401,F403

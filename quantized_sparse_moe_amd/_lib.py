@@ -30,6 +30,10 @@ MOE_DEVERR_TOKEN_ID = 1
 MOE_DEVERR_HASH_ID = 2
 MOE_DEVERR_EXPERT_ID = 4
 MOE_DEVERR_QUANT_INPUT = 8
+MOE_DEVERR_ROW_INDEX = 16
+
+MOE_DT = {"bf16": 0, "f32": 1, "f16": 2}
+MOE_ROWS = {"bucket": 0, "token": 1, "slot": 2}
 
 
 class QTensorC(Structure):
@@ -85,6 +89,17 @@ _SIGS = {
     "moe_mhc_sinkhorn": (c_int32, [c_void_p, c_int64, c_int32, c_int32, c_float, c_void_p, c_void_p]),
     "moe_quantize_affine": (c_int32, [c_void_p, c_int64, c_int32, c_int32, c_int32, c_void_p, c_void_p, c_void_p,
                                       c_void_p, c_void_p]),
+    "moe_quantize_block": (c_int32, [c_void_p, c_int32, c_int64, c_int64, c_int32, c_int32, c_int32, c_void_p,
+                                     c_void_p, c_void_p, c_void_p]),
+    "moe_swiglu_quantize_block": (c_int32, [c_void_p, c_int32, c_int64, c_int32, c_int32, c_void_p, c_void_p,
+                                            c_void_p, c_void_p]),
+    "moe_matmul_block": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_int32, c_int32,
+                                   c_void_p, c_void_p]),
+    "moe_grouped_matmul_block": (c_int32, [c_void_p] * 4 + [c_int32] * 5 + [c_void_p] * 2 + [c_int32] * 3
+                                 + [c_void_p] * 3),
+    "moe_grouped_matmul": (c_int32, [c_void_p] * 2 + [c_int32] * 6 + [c_void_p] * 2 + [c_int32] * 4 + [c_void_p] * 3),
+    "moe_grouped_matmul_dw": (c_int32, [c_void_p] * 2 + [c_int32] * 6 + [c_void_p] * 2 + [c_int32] * 3
+                              + [c_void_p] * 3),
     "moe_status_string": (c_char_p, [c_int32]),
     "moe_version": (c_char_p, []),
 }

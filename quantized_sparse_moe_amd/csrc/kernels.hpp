@@ -138,6 +138,49 @@ hipError_t launch_quantize_affine(const uint16_t* w, int64_t rows, int cols, int
 hipError_t launch_mhc_sinkhorn(const float* logits, int64_t T, int n, int iters, float eps, float* out,
                                hipStream_t s);
 
+// Block-scaled FP8 quantiser ---------------------------------------------------
+// Types as moe_dtype; x [matrices][rows][cols].
+hipError_t launch_quantize_block(const void* x, int dtype, int64_t matrices, int64_t rows, int cols, int block_rows,
+                                 int pow2, uint8_t* codes, float* scales, int32_t* err, hipStream_t s);
+hipError_t launch_swiglu_quantize_block(const void* gu, int dtype, int64_t rows, int inner, int pow2, uint8_t* codes,
+                                        float* scales, int32_t* err, hipStream_t s);
+
+// Products grouped by expert ----------------------------------------------------
+constexpr int kTypeE4m3 = 3;  // element type beside moe_dtype's, with scales
+
+// out[p][c] = sum_q r[p][q] * c[e(p)][c][q], or c[e(p)][q][c] when transposed.
+struct ProductArgs {
+  const void* r;           // rows: [T*k] or [T] (r_order) x Q
+  const float* r_scales;   // e4m3: [rows][ceil(Q / 128)]
+  const void* c;           // weights of E experts, [C][Q] or (transposed) [Q][C] each
+  const float* c_scales;   // e4m3: [E][ceil(C / 128)][ceil(Q / 128)]
+  int32_t type;            // of r and c
+  int32_t out_type;        // moe_dtype
+  int32_t T, k, E;
+  int32_t C, Q;            // output columns, contraction length
+  int32_t transposed;
+  const int32_t* offsets;  // null: one expert for all rows
+  const int32_t* perm;
+  int32_t r_order, out_order;
+  void* out;
+  int32_t* err;
+};
+hipError_t launch_product(const ProductArgs& a, hipStream_t s);
+
+// out[e][n][k] = sum over expert e's positions p of dy[p][n] * x[p][k].
+struct DwArgs {
+  const void* x;
+  const void* dy;
+  int32_t type, out_type;
+  int32_t T, k, E, N, K;
+  const int32_t* offsets;
+  const int32_t* perm;
+  int32_t x_order, dy_order;
+  void* out;
+  int32_t* err;
+};
+hipError_t launch_product_dw(const DwArgs& a, hipStream_t s);
+
 // Measurement kernels -----------------------------------------------------------
 // mode 0: read every byte of buf once (16 bytes per lane); 1: read the first
 // 32 bytes of every 128-byte line; 2: write every byte once.
