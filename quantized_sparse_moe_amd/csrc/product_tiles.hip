@@ -136,12 +136,14 @@ __global__ __launch_bounds__(WM* WN * 64) void k_tile_product(ProductArgs a, int
 #pragma unroll
     for (int q = 0; q < TC; ++q) acc[i][q] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // fragment addresses within a stage
+  // fragment addresses within a stage; row fragment i of this wave is the
+  // tile's fragment i * WM + wm, so that a short tile leaves both halves less
   int ra[2], ca[TC];
+  constexpr int RSTEP = WM * 16 * kStepBytes;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int piece = FP8 ? 2 * g + h : 4 * h + g;
-    ra[h] = (wm * TR * 16 + j) * kStepBytes + (piece ^ swz_r(j)) * 16;
+    ra[h] = (wm * 16 + j) * kStepBytes + (piece ^ swz_r(j)) * 16;
     const int cn = 16 * (j >> 2) + (j & 3);
     if constexpr (!CT) ca[h] = BM * kStepBytes + (wn * 64 + cn) * kStepBytes + (piece ^ swz_c(cn)) * 16;
   }
@@ -152,90 +154,186 @@ __global__ __launch_bounds__(WM* WN * 64) void k_tile_product(ProductArgs a, int
               (((wn * 64 + 16 * q) / 8 + ((j & 3) >> 1)) ^ swz_q(8 * g + (j >> 2))) * 16 + (j & 1) * 8;
   }
 
+  // The stage of step kb, once its loads have landed: the S - 2 steps behind
+  // it may be in flight, counted only if each issued its full number of loads.
+  auto arrive = [&](int kb) {
+    if (S > 2 && kb + S - 2 < full)
+      barrier_keep<(S - 2) * LOADS>();
+    else
+      barrier_keep<0>();
+    if (kb + S - 1 < steps) issue(kb + S - 1);
+  };
+  auto stage_of = [&](int kb) -> const char* { return smem + (kb % S) * STAGE; };
   float sbs = 0.0f;  // the weights' scales of 64 steps, one per lane
-  auto compute = [&](int kb) {
-    const char* st = smem + (kb % S) * STAGE;
-    if constexpr (FP8) {
-      if ((kb & 63) == 0) {
-        sbs = csc[min(kb + lane, qb - 1)];
-        asm volatile("" ::"v"(sbs));  // wait for it here, not in every step
-      }
-      const float sb = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(sbs), kb & 63));
-      i32x8_t cf[TC];
+  auto weight_scale = [&](int kb) {
+    if ((kb & 63) == 0) {
+      sbs = csc[min(kb + lane, qb - 1)];
+      asm volatile("" ::"v"(sbs));  // wait for it here, not in every step
+    }
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(sbs), kb & 63));
+  };
+  auto frag8 = [&](const char* at0, const char* at1) {
+    return __builtin_bit_cast(i32x8_t, __builtin_shufflevector(lds16(at0), lds16(at1), 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+
+  // Each step's products over the first 2 * NI row fragments (a tile with few
+  // rows skips the others). Fragments are read from LDS one group ahead of
+  // their products, across the barrier too: the last group's products run
+  // while the next step's first fragments are on their way.
+  auto run_steps = [&](auto ni) {
+    constexpr int NI = decltype(ni)::value;
+    if constexpr (TYPE == kE4m3Wide) {
+      for (int kb = 0; kb < steps; ++kb) {
+        arrive(kb);
+        const char* st = stage_of(kb);
+        const float sb = weight_scale(kb);
+        const float* ss = reinterpret_cast<const float*>(st + (BM + BN) * kStepBytes) + wm * 16 + j;
+        i32x8_t cf[TC];
 #pragma unroll
-      for (int q = 0; q < TC; ++q) {
-        u32x4_t lo = lds16(st + ca[0] + q * 512), hi = lds16(st + ca[1] + q * 512);
-        cf[q] = __builtin_bit_cast(i32x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-      }
-      const float* ss = reinterpret_cast<const float*>(st + (BM + BN) * kStepBytes) + wm * TR * 16 + j;
+        for (int q = 0; q < TC; ++q) cf[q] = frag8(st + ca[0] + q * 512, st + ca[1] + q * 512);
 #pragma unroll
-      for (int i = 0; i < TR; ++i) {
-        u32x4_t lo = lds16(st + ra[0] + i * 2048), hi = lds16(st + ra[1] + i * 2048);
-        const i32x8_t rf = __builtin_bit_cast(i32x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-        const float s = ss[i * 16] * sb;
-        u32x4_t rw[4];
-        if constexpr (TYPE == kE4m3Wide) {
+        for (int i = 0; i < 2 * NI; ++i) {
+          const i32x8_t rf = frag8(st + ra[0] + i * RSTEP, st + ra[1] + i * RSTEP);
+          const float sc = ss[i * WM * 16] * sb;
+          u32x4_t rw[4];
 #pragma unroll
           for (int v = 0; v < 4; ++v) rw[v] = e4m3_to_bf16x8(rf[2 * v], rf[2 * v + 1]);
-        }
 #pragma unroll
-        for (int q = 0; q < TC; ++q) {
-          f32x4_t part = {0.0f, 0.0f, 0.0f, 0.0f};
-          if constexpr (TYPE == kE4m3Wide) {
+          for (int q = 0; q < TC; ++q) {
+            f32x4_t part = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int v = 0; v < 4; ++v)
               part = mma16<0>(e4m3_to_bf16x8(cf[q][2 * v], cf[q][2 * v + 1]), rw[v], part);
-          } else {
-            part = mma_fp8(cf[q], rf);
-          }
 #pragma unroll
-          for (int v = 0; v < 4; ++v) acc[i][q][v] = fmaf(part[v], s, acc[i][q][v]);
+            for (int v = 0; v < 4; ++v) acc[i][q][v] = fmaf(part[v], sc, acc[i][q][v]);
+          }
         }
       }
-    } else {
+    } else if constexpr (FP8) {
+      // a block's 128 products are summed by one instruction; its scale is
+      // applied one fragment later, beside the next fragment's instructions
+      constexpr int N = 2 * NI;
+      i32x8_t cf[TC], rf[2];
+      f32x4_t part[2][TC];
+      float sc[2] = {0.0f, 0.0f}, done = 0.0f;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        u32x4_t cf[TC];
+      for (int q = 0; q < TC; ++q) part[1][q] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      auto rows = [&](const char* st, int i, int buf) {
+        rf[buf] = frag8(st + ra[0] + i * RSTEP, st + ra[1] + i * RSTEP);
+        sc[buf] = reinterpret_cast<const float*>(st + (BM + BN) * kStepBytes)[(i * WM + wm) * 16 + j];
+      };
+      auto scale = [&](int i, int buf) {
+#pragma unroll
+        for (int q = 0; q < TC; ++q)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[i][q][v] = fmaf(part[buf][q][v], done, acc[i][q][v]);
+        // done here: the compiler would put them off to behind the barrier, with all partial sums in registers
+#pragma unroll
+        for (int q = 0; q < TC; ++q) asm volatile("" : "+v"(acc[i][q]));
+      };
+      if (steps > 0) {
+        arrive(0);
+#pragma unroll
+        for (int q = 0; q < TC; ++q) cf[q] = frag8(smem + ca[0] + q * 512, smem + ca[1] + q * 512);
+        rows(smem, 0, 0);
+      }
+      auto step = [&](int kb, auto more_) {
+        constexpr bool MORE = decltype(more_)::value;
+        const float sb = weight_scale(kb);
+        const char* st = stage_of(kb);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float mine = sc[i & 1] * sb;
+          if (i + 1 < N) rows(st, i + 1, (i + 1) & 1);
+#pragma unroll
+          for (int q = 0; q < TC; ++q) part[i & 1][q] = mma_fp8(cf[q], rf[i & 1]);
+          if constexpr (MORE) {
+            if (i + 1 == N) {
+              __builtin_amdgcn_sched_barrier(0);  // the column fragments' registers are free from here on
+              arrive(kb + 1);
+              const char* next = stage_of(kb + 1);
+#pragma unroll
+              for (int q = 0; q < TC; ++q) cf[q] = frag8(next + ca[0] + q * 512, next + ca[1] + q * 512);
+              rows(next, 0, 0);
+            }
+          }
+          scale((i + N - 1) % N, (i + 1) & 1);
+          done = mine;
+          __builtin_amdgcn_sched_barrier(0);  // or fragments are read far ahead, into registers that spill
+        }
+      };
+      for (int kb = 0; kb + 1 < steps; ++kb) step(kb, std::true_type{});
+      if (steps > 0) step(steps - 1, std::false_type{});
+      scale(N - 1, 1);
+    } else {
+      constexpr int N = 2 * NI;  // groups of 2 row fragments in a step: NI for each half of its inputs
+      u32x4_t cf[2][TC], rf[2][2];
+      auto cols = [&](const char* st, auto h_) {
+        constexpr int H = decltype(h_)::value;
         if constexpr (CT) {
           int at[TC];
 #pragma unroll
           for (int q = 0; q < TC; ++q) at[q] = lds_address(st) + ca[q];
-          if (h == 0)
-            lds_tr_x4<0, 8 * BN>(at, cf);
-          else
-            lds_tr_x4<64 * BN, 72 * BN>(at, cf);
+          lds_tr_x4<H * 64 * BN, H * 64 * BN + 8 * BN>(at, cf[H]);
         } else {
 #pragma unroll
-          for (int q = 0; q < TC; ++q) cf[q] = lds16(st + ca[h] + q * 512);
+          for (int q = 0; q < TC; ++q) cf[H][q] = lds16(st + ca[H] + q * 512);
         }
+      };
+      auto rows = [&](const char* st, int it) {
 #pragma unroll
-        for (int i = 0; i < TR; ++i) {
-          const u32x4_t rf = lds16(st + ra[h] + i * 2048);
-#pragma unroll
-          for (int q = 0; q < TC; ++q) acc[i][q] = mma16<TYPE>(cf[q], rf, acc[i][q]);
-        }
+        for (int v = 0; v < 2; ++v) rf[it & 1][v] = lds16(st + ra[it / NI] + ((it % NI) * 2 + v) * RSTEP);
+      };
+      const std::integral_constant<int, 0> first;
+      const std::integral_constant<int, 1> second;
+      if (steps > 0) {
+        arrive(0);
+        cols(smem, first);
+        rows(smem, 0);
       }
+      auto step = [&](int kb, auto more_) {
+        const char* st = stage_of(kb);
+#pragma unroll
+        for (int it = 0; it < N; ++it) {
+          if (it + 1 < N) {
+            if (it + 1 == NI) cols(st, second);
+            rows(st, it + 1);
+          } else if constexpr (decltype(more_)::value) {
+            arrive(kb + 1);
+            cols(stage_of(kb + 1), first);
+            rows(stage_of(kb + 1), 0);
+          }
+#pragma unroll
+          for (int v = 0; v < 2; ++v)
+#pragma unroll
+            for (int q = 0; q < TC; ++q) {
+              f32x4_t& c = acc[(it % NI) * 2 + v][q];
+              c = mma16<TYPE>(cf[it / NI][q], rf[it & 1][v], c);
+            }
+        }
+      };
+      for (int kb = 0; kb + 1 < steps; ++kb) step(kb, std::true_type{});
+      if (steps > 0) step(steps - 1, std::false_type{});
     }
   };
 
 #pragma unroll
   for (int s = 0; s < S - 1; ++s)
     if (s < steps) issue(s);
-  for (int kb = 0; kb < steps; ++kb) {
-    // step kb has landed: the S - 2 steps behind it may be in flight, counted
-    // only if each issued its full number of loads
-    if (S > 2 && kb + S - 2 < full)
-      barrier_keep<(S - 2) * LOADS>();
-    else
-      barrier_keep<0>();
-    if (kb + S - 1 < steps) issue(kb + S - 1);
-    compute(kb);
-  }
+  const int groups = (t.rows + 32 * WM - 1) / (32 * WM);
+  if (TR >= 8 && groups >= 4)
+    run_steps(std::integral_constant<int, TR / 2>{});
+  else if (TR >= 8 && groups == 3)
+    run_steps(std::integral_constant<int, TR >= 8 ? 3 : 1>{});
+  else if (TR >= 4 && groups >= 2)
+    run_steps(std::integral_constant<int, TR >= 4 ? 2 : 1>{});
+  else
+    run_steps(std::integral_constant<int, 1>{});
 
   const int osize = a.out_type == 1 ? 4 : 2;
 #pragma unroll
   for (int i = 0; i < TR; ++i) {
-    const int r = wm * TR * 16 + 16 * i + j;
+    const int r = (i * WM + wm) * 16 + j;
     if (r >= t.rows) continue;
     const int row = row_of(a.perm, a.out_order, a.k, n, t.first + r, a.err);
     if (row < 0) continue;
@@ -265,10 +363,10 @@ __global__ __launch_bounds__(WM* WN * 64) void k_tile_dw(DwArgs a, int64_t pairs
   constexpr int S = 2;
   constexpr int NT = WM * WN * 64;
   constexpr int TR = BM / WM / 16, TC = 4;
-  constexpr int NR = BM * 8 / NT, NC = BN * 8 / NT;
-  constexpr int RPR = BM / 8, CPR = BN / 8;  // 16-byte pieces of a contraction row
+  constexpr int NR = BM * 8 / NT;
+  constexpr int RPR = BM / 8;  // 16-byte pieces of a contraction row
   constexpr int STAGE = (BM + BN) * kStepBytes;
-  static_assert(BN == WN * 64 && TR % 4 == 0 && BM >= 128 && BN >= 128, "tile shape");
+  static_assert(BN == WN * 64 && (TR == 4 || TR == 8) && BM >= 128 && BN >= 128, "tile shape");
   __shared__ __attribute__((aligned(16))) char smem[S * STAGE];
 
   const int64_t pair = pair_of_block(run);
@@ -287,30 +385,23 @@ __global__ __launch_bounds__(WM* WN * 64) void k_tile_dw(DwArgs a, int64_t pairs
   const int g = lane >> 4, j = lane & 15;
   const int steps = (count + 63) / 64, full = count / 64;
 
-  int rcol[NR], ccol[NC];
+  int rcol[NR], ccol[NR];
 #pragma unroll
   for (int i = 0; i < NR; ++i) {
-    const int col = r0 + ((tid % RPR) ^ swz_q(i * (NT / RPR) + tid / RPR)) * 8;
-    rcol[i] = col < a.N ? col : r0;
+    const int col = ((tid % RPR) ^ swz_q(i * (NT / RPR) + tid / RPR)) * 8;
+    rcol[i] = r0 + col < a.N ? r0 + col : r0;
+    ccol[i] = c0 + col < a.K ? c0 + col : c0;
   }
-#pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    const int col = c0 + ((tid % CPR) ^ swz_q(i * (NT / CPR) + tid / CPR)) * 8;
-    ccol[i] = col < a.K ? col : c0;
-  }
-  int rrow[NR], crow[NC];  // source rows of the next step to be issued
+  // perm's entries of the step to be issued next, one per 16-byte piece; the
+  // two operands' pieces lie on the same contraction rows
+  static_assert(BM == BN, "one look-up for both operands");
+  const bool bucketed = a.x_order == kBucket && a.dy_order == kBucket;
+  const double per_k = 1.0 / a.k;  // (a + 1/2) / k in 64 bits floors right for every a < 2^31
+  int raw[NR];
   auto look_up = [&](int kb) {
-    if (kb >= steps) return;
+    if (bucketed || kb >= steps) return;
 #pragma unroll
-    for (int i = 0; i < NR; ++i) {
-      const int p = lo + min(kb * 64 + i * (NT / RPR) + tid / RPR, count - 1);
-      rrow[i] = max(row_of(a.perm, a.dy_order, a.k, n, p, a.err), 0);
-    }
-#pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      const int p = lo + min(kb * 64 + i * (NT / CPR) + tid / CPR, count - 1);
-      crow[i] = max(row_of(a.perm, a.x_order, a.k, n, p, a.err), 0);
-    }
+    for (int i = 0; i < NR; ++i) raw[i] = a.perm[lo + min(kb * 64 + i * (NT / RPR) + tid / RPR, count - 1)];
   };
   auto issue = [&](int kb) {
     char* sr = smem + (kb % S) * STAGE + wave * 1024;
@@ -320,17 +411,25 @@ __global__ __launch_bounds__(WM* WN * 64) void k_tile_dw(DwArgs a, int64_t pairs
     const u32x4_t zero = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
-      if (kb < full || kb * 64 + i * (NT / RPR) + tid / RPR < count)
-        load_lds16(dy + static_cast<int64_t>(rrow[i]) * a.N + rcol[i], sr + i * NT * 16);
-      else
+      const int at = kb * 64 + i * (NT / RPR) + tid / RPR;
+      const bool in = kb < full || at < count;
+      int rd = lo + at, rx = rd;
+      if (!bucketed && in) {
+        if (raw[i] < 0 || raw[i] >= n) {
+          set_device_error(a.err, 16);
+          raw[i] = 0;
+        }
+        if (a.dy_order == kSlot) rd = raw[i];
+        if (a.x_order == kSlot) rx = raw[i];
+        if (a.x_order == kToken) rx = static_cast<int>((raw[i] + 0.5) * per_k);
+      }
+      if (in) {
+        load_lds16(dy + static_cast<int64_t>(rd) * a.N + rcol[i], sr + i * NT * 16);
+        load_lds16(x + static_cast<int64_t>(rx) * a.K + ccol[i], sc + i * NT * 16);
+      } else {
         *reinterpret_cast<u32x4_t*>(sr + i * NT * 16 + lane * 16) = zero;
-    }
-#pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      if (kb < full || kb * 64 + i * (NT / CPR) + tid / CPR < count)
-        load_lds16(x + static_cast<int64_t>(crow[i]) * a.K + ccol[i], sc + i * NT * 16);
-      else
         *reinterpret_cast<u32x4_t*>(sc + i * NT * 16 + lane * 16) = zero;
+      }
     }
   };
 
@@ -350,35 +449,74 @@ __global__ __launch_bounds__(WM* WN * 64) void k_tile_dw(DwArgs a, int64_t pairs
     ca[i] = lds_address(smem) + BM * kStepBytes + q0 * BN * 2 + (((wn * 64 + 16 * i) / 8 + ((j & 3) >> 1)) ^ sw) * 16 +
             (j & 1) * 8;
 
-  auto half = [&](int st, auto h_) {
+  // as in the product: groups of 4 row fragments, each read while the group
+  // before it is multiplied, across the barrier too
+  constexpr int G = TR / 4;  // groups of each half of a step's inputs
+  u32x4_t cf[2][TC], rf[2][4];
+  auto cols = [&](int st, auto h_) {
     constexpr int H = decltype(h_)::value;
-    u32x4_t cf[TC];
     int at4[4];
 #pragma unroll
     for (int q = 0; q < TC; ++q) at4[q] = ca[q] + st;
-    lds_tr_x4<H * 64 * BN, H * 64 * BN + 8 * BN>(at4, cf);
+    lds_tr_x4<H * 64 * BN, H * 64 * BN + 8 * BN>(at4, cf[H]);
+  };
+  auto rows = [&](int st, auto it_) {
+    constexpr int IT = decltype(it_)::value, H = IT / G;
+    int at4[4];
 #pragma unroll
-    for (int i = 0; i < TR; i += 4) {
-      u32x4_t rf[4];
+    for (int q = 0; q < 4; ++q) at4[q] = ra[IT % G * 4 + q] + st;
+    lds_tr_x4<H * 64 * BM, H * 64 * BM + 8 * BM>(at4, rf[IT & 1]);
+  };
+  auto products = [&](int it) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) at4[q] = ra[i + q] + st;
-      lds_tr_x4<H * 64 * BM, H * 64 * BM + 8 * BM>(at4, rf);
+    for (int v = 0; v < 4; ++v)
 #pragma unroll
-      for (int v = 0; v < 4; ++v)
-#pragma unroll
-        for (int q = 0; q < TC; ++q) acc[i + v][q] = mma16<TYPE>(cf[q], rf[v], acc[i + v][q]);
+      for (int q = 0; q < TC; ++q) {
+        f32x4_t& c = acc[it % G * 4 + v][q];
+        c = mma16<TYPE>(cf[it / G][q], rf[it & 1][v], c);
+      }
+  };
+  const std::integral_constant<int, 0> i0;
+  const std::integral_constant<int, 1> i1;
+  const std::integral_constant<int, G == 2 ? 2 : 0> i2;
+  const std::integral_constant<int, G == 2 ? 3 : 1> i3;
+  auto arrive = [&](int kb) {
+    barrier_keep<0>();
+    if (kb + 1 < steps) {
+      issue(kb + 1);
+      look_up(kb + 2);
     }
   };
 
   look_up(0);
-  if (steps > 0) issue(0);
-  look_up(1);
+  if (steps > 0) {
+    issue(0);
+    look_up(1);
+    arrive(0);
+    cols(0, i0);
+    rows(0, i0);
+  }
   for (int kb = 0; kb < steps; ++kb) {
-    barrier_keep<0>();
-    if (kb + 1 < steps) issue(kb + 1);
-    look_up(kb + 2);
-    half((kb % S) * STAGE, std::integral_constant<int, 0>{});
-    half((kb % S) * STAGE, std::integral_constant<int, 1>{});
+    const int st = (kb % S) * STAGE, next = ((kb + 1) % S) * STAGE;
+    if constexpr (G == 2) {
+      rows(st, i1);
+      products(0);
+      cols(st, i1);
+      rows(st, i2);
+      products(1);
+      rows(st, i3);
+      products(2);
+    } else {
+      cols(st, i1);
+      rows(st, i1);
+      products(0);
+    }
+    if (kb + 1 < steps) {
+      arrive(kb + 1);
+      cols(next, i0);
+      rows(next, i0);
+    }
+    products(2 * G - 1);
   }
 
   const int osize = a.out_type == 1 ? 4 : 2;
@@ -413,7 +551,8 @@ template <int TYPE, bool CT>
 hipError_t pick_tiles(const ProductArgs& a, hipStream_t s) {
   const int64_t n = static_cast<int64_t>(a.T) * a.k;
   const int64_t mean = n / a.E;
-  if (mean >= 192) return launch_tiles<TYPE, 256, 256, 2, 4, 2, CT>(a, s);
+  if constexpr (TYPE != kE4m3Wide)
+    if (mean >= 192) return launch_tiles<TYPE, 256, 256, 2, 4, 2, CT>(a, s);
   if (mean >= 48) return launch_tiles<TYPE, 128, 256, 2, 4, 3, CT>(a, s);
   return launch_tiles<TYPE, 64, 128, 2, 2, 3, CT>(a, s);
 }
