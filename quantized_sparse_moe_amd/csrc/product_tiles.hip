@@ -41,13 +41,13 @@ __global__ __launch_bounds__(WM* WN * 64) void k_tile_product(ProductArgs a, int
   constexpr int ESIZE = FP8 ? 1 : 2;
   constexpr int NT = WM * WN * 64;
   constexpr int TR = BM / WM / 16;   // row fragments of a wave
-  constexpr int TC = 4;              // column fragments
+  constexpr int TC = BN / WN / 16;   // column fragments
   constexpr int NR = BM * 8 / NT, NC = BN * 8 / NT;
   constexpr int SCALES = FP8 ? WM * WN * 256 : 0;
   constexpr int STAGE = (BM + BN) * kStepBytes + SCALES;
   constexpr int LOADS = NR + NC + (FP8 ? 1 : 0);
-  static_assert(BN == WN * 64 && NR >= 1 && NC >= 1 && NT % 256 == 0, "tile shape");
-  static_assert(!(FP8 && CT), "FP8 weights have the contraction contiguous");
+  static_assert(TC % 4 == 0 && NR >= 1 && NC >= 1 && NT % 256 == 0, "tile shape");
+  static_assert(!FP8 || (!CT && TC == 4), "FP8 weights have the contraction contiguous, one scale block per wave");
   __shared__ __attribute__((aligned(16))) char smem[S * STAGE];
 
   const int n = a.T * a.k;
@@ -99,17 +99,25 @@ __global__ __launch_bounds__(WM* WN * 64) void k_tile_product(ProductArgs a, int
           (static_cast<int64_t>(t.e) * ((a.C + 127) / 128) + min((c0 + wn * 64) / 128, (a.C - 1) / 128)) * qb;
   }
 
-  auto issue = [&](int kb) {
+  auto issue_full = [&](int kb) {
     char* st = smem + (kb % S) * STAGE;
     char* sr = st + wave * 1024;
     char* sc = sr + BM * kStepBytes;
     const char* cb = cbase + kb * cstep;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) load_lds16(rp[i] + kb * kStepBytes, sr + i * NT * 16);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) load_lds16(cb + co[i], sc + i * NT * 16);
+    if constexpr (FP8) load_lds4(sp + kb, st + (BM + BN) * kStepBytes + wave * 256);
+  };
+  auto issue = [&](int kb) {
     if (kb < full) {
-#pragma unroll
-      for (int i = 0; i < NR; ++i) load_lds16(rp[i] + kb * kStepBytes, sr + i * NT * 16);
-#pragma unroll
-      for (int i = 0; i < NC; ++i) load_lds16(cb + co[i], sc + i * NT * 16);
+      issue_full(kb);
     } else {  // the last step of a ragged contraction: zeros behind its end
+      char* st = smem + (kb % S) * STAGE;
+      char* sr = st + wave * 1024;
+      char* sc = sr + BM * kStepBytes;
+      const char* cb = cbase + kb * cstep;
       const u32x4_t zero = {0, 0, 0, 0};
       const int rest = qbytes - kb * kStepBytes;
 #pragma unroll
@@ -126,8 +134,8 @@ __global__ __launch_bounds__(WM* WN * 64) void k_tile_product(ProductArgs a, int
         else
           *reinterpret_cast<u32x4_t*>(sc + i * NT * 16 + lane * 16) = zero;
       }
+      if constexpr (FP8) load_lds4(sp + kb, st + (BM + BN) * kStepBytes + wave * 256);
     }
-    if constexpr (FP8) load_lds4(sp + kb, st + (BM + BN) * kStepBytes + wave * 256);
   };
 
   f32x4_t acc[TR][TC];
@@ -145,13 +153,13 @@ __global__ __launch_bounds__(WM* WN * 64) void k_tile_product(ProductArgs a, int
     const int piece = FP8 ? 2 * g + h : 4 * h + g;
     ra[h] = (wm * 16 + j) * kStepBytes + (piece ^ swz_r(j)) * 16;
     const int cn = 16 * (j >> 2) + (j & 3);
-    if constexpr (!CT) ca[h] = BM * kStepBytes + (wn * 64 + cn) * kStepBytes + (piece ^ swz_c(cn)) * 16;
+    if constexpr (!CT) ca[h] = BM * kStepBytes + (wn * TC * 16 + cn) * kStepBytes + (piece ^ swz_c(cn)) * 16;
   }
   if constexpr (CT) {
 #pragma unroll
     for (int q = 0; q < TC; ++q)
       ca[q] = BM * kStepBytes + (8 * g + (j >> 2)) * BN * 2 +
-              (((wn * 64 + 16 * q) / 8 + ((j & 3) >> 1)) ^ swz_q(8 * g + (j >> 2))) * 16 + (j & 1) * 8;
+              (((wn * TC * 16 + 16 * q) / 8 + ((j & 3) >> 1)) ^ swz_q(8 * g + (j >> 2))) * 16 + (j & 1) * 8;
   }
 
   // The stage of step kb, once its loads have landed: the S - 2 steps behind
@@ -237,8 +245,8 @@ __global__ __launch_bounds__(WM* WN * 64) void k_tile_product(ProductArgs a, int
         for (int q = 0; q < TC; ++q) cf[q] = frag8(smem + ca[0] + q * 512, smem + ca[1] + q * 512);
         rows(smem, 0, 0);
       }
-      auto step = [&](int kb, auto more_) {
-        constexpr bool MORE = decltype(more_)::value;
+      auto step = [&](int kb, auto inner_) {
+        constexpr bool INNER = decltype(inner_)::value;
         const float sb = weight_scale(kb);
         const char* st = stage_of(kb);
 #pragma unroll
@@ -247,10 +255,15 @@ __global__ __launch_bounds__(WM* WN * 64) void k_tile_product(ProductArgs a, int
           if (i + 1 < N) rows(st, i + 1, (i + 1) & 1);
 #pragma unroll
           for (int q = 0; q < TC; ++q) part[i & 1][q] = mma_fp8(cf[q], rf[i & 1]);
-          if constexpr (MORE) {
-            if (i + 1 == N) {
+          if (i + 1 == N) {
+            if (INNER || kb + 1 < steps) {
               __builtin_amdgcn_sched_barrier(0);  // the column fragments' registers are free from here on
-              arrive(kb + 1);
+              if constexpr (INNER) {
+                barrier_keep<(S - 2) * LOADS>();
+                issue_full(kb + S);
+              } else {
+                arrive(kb + 1);
+              }
               const char* next = stage_of(kb + 1);
 #pragma unroll
               for (int q = 0; q < TC; ++q) cf[q] = frag8(next + ca[0] + q * 512, next + ca[1] + q * 512);
@@ -262,8 +275,9 @@ __global__ __launch_bounds__(WM* WN * 64) void k_tile_product(ProductArgs a, int
           __builtin_amdgcn_sched_barrier(0);  // or fragments are read far ahead, into registers that spill
         }
       };
-      for (int kb = 0; kb + 1 < steps; ++kb) step(kb, std::true_type{});
-      if (steps > 0) step(steps - 1, std::false_type{});
+      int kb = 0;
+      for (; kb + S < full; ++kb) step(kb, std::true_type{});
+      for (; kb < steps; ++kb) step(kb, std::false_type{});
       scale(N - 1, 1);
     } else {
       constexpr int N = 2 * NI;  // groups of 2 row fragments in a step: NI for each half of its inputs
@@ -271,13 +285,19 @@ __global__ __launch_bounds__(WM* WN * 64) void k_tile_product(ProductArgs a, int
       auto cols = [&](const char* st, auto h_) {
         constexpr int H = decltype(h_)::value;
         if constexpr (CT) {
-          int at[TC];
 #pragma unroll
-          for (int q = 0; q < TC; ++q) at[q] = lds_address(st) + ca[q];
-          lds_tr_x4<H * 64 * BN, H * 64 * BN + 8 * BN>(at, cf[H]);
+          for (int p = 0; p < TC; p += 4) {
+            int at[4];
+            u32x4_t f[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) at[q] = lds_address(st) + ca[p + q];
+            lds_tr_x4<H * 64 * BN, H * 64 * BN + 8 * BN>(at, f);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) cf[H][p + q] = f[q];
+          }
         } else {
 #pragma unroll
-          for (int q = 0; q < TC; ++q) cf[H][q] = lds16(st + ca[H] + q * 512);
+          for (int q = 0; q < TC; ++q) cf[H][q] = lds16(st + ca[H] + (q >> 2) * 64 * kStepBytes + (q & 3) * 512);
         }
       };
       auto rows = [&](const char* st, int it) {
@@ -291,15 +311,22 @@ __global__ __launch_bounds__(WM* WN * 64) void k_tile_product(ProductArgs a, int
         cols(smem, first);
         rows(smem, 0);
       }
-      auto step = [&](int kb, auto more_) {
+      // INNER: the step to be issued is whole, so that nothing branches
+      auto step = [&](int kb, auto inner_) {
+        constexpr bool INNER = decltype(inner_)::value;
         const char* st = stage_of(kb);
 #pragma unroll
         for (int it = 0; it < N; ++it) {
           if (it + 1 < N) {
             if (it + 1 == NI) cols(st, second);
             rows(st, it + 1);
-          } else if constexpr (decltype(more_)::value) {
-            arrive(kb + 1);
+          } else if (INNER || kb + 1 < steps) {
+            if constexpr (INNER) {
+              barrier_keep<(S - 2) * LOADS>();
+              issue_full(kb + S);
+            } else {
+              arrive(kb + 1);
+            }
             cols(stage_of(kb + 1), first);
             rows(stage_of(kb + 1), 0);
           }
@@ -312,8 +339,9 @@ __global__ __launch_bounds__(WM* WN * 64) void k_tile_product(ProductArgs a, int
             }
         }
       };
-      for (int kb = 0; kb + 1 < steps; ++kb) step(kb, std::true_type{});
-      if (steps > 0) step(steps - 1, std::false_type{});
+      int kb = 0;
+      for (; kb + S < full; ++kb) step(kb, std::true_type{});
+      for (; kb < steps; ++kb) step(kb, std::false_type{});
     }
   };
 
@@ -341,13 +369,13 @@ __global__ __launch_bounds__(WM* WN * 64) void k_tile_product(ProductArgs a, int
     if constexpr (CT) {
 #pragma unroll
       for (int q = 0; q < TC; ++q) {
-        const int c = c0 + wn * 64 + 16 * q + 4 * g;
+        const int c = c0 + (wn * TC + q) * 16 + 4 * g;
         if (c < a.C) store4(o + static_cast<int64_t>(c) * osize, a.out_type, acc[i][q]);
       }
     } else {
 #pragma unroll
       for (int q = 0; q < TC; q += 2) {
-        const int c = c0 + wn * 64 + 16 * g + 4 * q;
+        const int c = c0 + wn * TC * 16 + (q >> 2) * 64 + 16 * g + 4 * (q & 3);
         if (c < a.C) store8(o + static_cast<int64_t>(c) * osize, a.out_type, acc[i][q], acc[i][q + 1]);
       }
     }
@@ -552,7 +580,11 @@ hipError_t pick_tiles(const ProductArgs& a, hipStream_t s) {
   const int64_t n = static_cast<int64_t>(a.T) * a.k;
   const int64_t mean = n / a.E;
   if constexpr (TYPE != kE4m3Wide)
+#ifdef TRY4
+    if (mean >= 192) return launch_tiles<TYPE, 256, 256, 2, TYPE == kTypeE4m3 || CT ? 4 : 2, 2, CT>(a, s);
+#else
     if (mean >= 192) return launch_tiles<TYPE, 256, 256, 2, 4, 2, CT>(a, s);
+#endif
   if (mean >= 48) return launch_tiles<TYPE, 128, 256, 2, 4, 3, CT>(a, s);
   return launch_tiles<TYPE, 64, 128, 2, 2, 3, CT>(a, s);
 }
