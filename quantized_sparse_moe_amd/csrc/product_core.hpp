@@ -136,6 +136,7 @@ __device__ __forceinline__ void store4(char* p, int out_type, f32x4_t v) {
     *reinterpret_cast<uint2*>(p) = u;
   }
 }
+
 __device__ __forceinline__ void store8(char* p, int out_type, f32x4_t v, f32x4_t w) {
   if (out_type == 1) {
     reinterpret_cast<f32x4_t*>(p)[0] = v;
