@@ -150,7 +150,7 @@ __global__ __launch_bounds__(WM* WN * 64) void k_tile_product(ProductArgs a, int
   constexpr int RSTEP = WM * 16 * kStepBytes;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int piece = FP8 ? 2 * g + h : 4 * h + g;
+    const int piece = 4 * h + g;
     ra[h] = (wm * 16 + j) * kStepBytes + (piece ^ swz_r(j)) * 16;
     const int cn = 16 * (j >> 2) + (j & 3);
     if constexpr (!CT) ca[h] = BM * kStepBytes + (wn * TC * 16 + cn) * kStepBytes + (piece ^ swz_c(cn)) * 16;
