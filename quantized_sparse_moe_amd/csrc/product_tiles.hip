@@ -219,58 +219,62 @@ __global__ __launch_bounds__(WM* WN * 64) void k_tile_product(ProductArgs a, int
       }
     } else if constexpr (FP8) {
       // a block's 128 products are summed by one instruction; its scale is
-      // applied one fragment later, beside the next fragment's instructions
-      constexpr int N = 2 * NI;
-      i32x8_t cf[TC], rf[2];
-      f32x4_t part[2][TC];
-      float sc[2] = {0.0f, 0.0f}, done = 0.0f;
+      // applied one fragment later, just before the next sum takes its place
+      constexpr int N = 2 * NI;             // row fragments
+      constexpr int NB = N == 4 ? 4 : 3;    // their buffers: fragment 0's is free when the last is multiplied
+      i32x8_t cf[TC], rf[NB];
+      f32x4_t part[TC];
+      float sc[NB], done = 0.0f;
 #pragma unroll
-      for (int q = 0; q < TC; ++q) part[1][q] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-      auto rows = [&](const char* st, int i, int buf) {
-        rf[buf] = frag8(st + ra[0] + i * RSTEP, st + ra[1] + i * RSTEP);
-        sc[buf] = reinterpret_cast<const float*>(st + (BM + BN) * kStepBytes)[(i * WM + wm) * 16 + j];
+      for (int q = 0; q < TC; ++q) part[q] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      auto cols = [&](const char* st, int q) { cf[q] = frag8(st + ca[0] + q * 512, st + ca[1] + q * 512); };
+      auto rows = [&](const char* st, int i) {
+        rf[i % NB] = frag8(st + ra[0] + i * RSTEP, st + ra[1] + i * RSTEP);
+        sc[i % NB] = reinterpret_cast<const float*>(st + (BM + BN) * kStepBytes)[(i * WM + wm) * 16 + j];
       };
-      auto scale = [&](int i, int buf) {
+      auto scale = [&](int i, int q) {
 #pragma unroll
-        for (int q = 0; q < TC; ++q)
-#pragma unroll
-          for (int v = 0; v < 4; ++v) acc[i][q][v] = fmaf(part[buf][q][v], done, acc[i][q][v]);
-        // done here: the compiler would put them off to behind the barrier, with all partial sums in registers
-#pragma unroll
-        for (int q = 0; q < TC; ++q) asm volatile("" : "+v"(acc[i][q]));
+        for (int v = 0; v < 4; ++v) acc[i][q][v] = fmaf(part[q][v], done, acc[i][q][v]);
+        // done here: the compiler would put them off to behind the barrier, with all sums in registers
+        asm volatile("" : "+v"(acc[i][q]));
       };
       if (steps > 0) {
         arrive(0);
 #pragma unroll
-        for (int q = 0; q < TC; ++q) cf[q] = frag8(smem + ca[0] + q * 512, smem + ca[1] + q * 512);
-        rows(smem, 0, 0);
+        for (int q = 0; q < TC; ++q) cols(smem, q);
+        rows(smem, 0);
       }
+      // INNER: the step to be issued is whole, so that nothing branches
       auto step = [&](int kb, auto inner_) {
         constexpr bool INNER = decltype(inner_)::value;
+        const bool more = INNER || kb + 1 < steps;
         const float sb = weight_scale(kb);
         const char* st = stage_of(kb);
+        const char* next = stage_of(kb + 1);
+        rows(st, 1);
+        if (N > 2) rows(st, 2);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          const float mine = sc[i & 1] * sb;
-          if (i + 1 < N) rows(st, i + 1, (i + 1) & 1);
-#pragma unroll
-          for (int q = 0; q < TC; ++q) part[i & 1][q] = mma_fp8(cf[q], rf[i & 1]);
-          if (i + 1 == N) {
-            if (INNER || kb + 1 < steps) {
-              __builtin_amdgcn_sched_barrier(0);  // the column fragments' registers are free from here on
-              if constexpr (INNER) {
-                barrier_keep<(S - 2) * LOADS>();
-                issue_full(kb + S);
-              } else {
-                arrive(kb + 1);
-              }
-              const char* next = stage_of(kb + 1);
-#pragma unroll
-              for (int q = 0; q < TC; ++q) cf[q] = frag8(next + ca[0] + q * 512, next + ca[1] + q * 512);
-              rows(next, 0, 0);
+          const float mine = sc[i % NB] * sb;
+          if (i > 0 && i + 2 < N) rows(st, i + 2);
+          if (i == N - 2 && more) {
+            if constexpr (INNER) {
+              barrier_keep<(S - 2) * LOADS>();
+              issue_full(kb + S);
+            } else {
+              arrive(kb + 1);
             }
           }
-          scale((i + N - 1) % N, (i + 1) & 1);
+          if (i == N - 1 && more) rows(next, 0);
+#pragma unroll
+          for (int q = 0; q < TC; ++q) {
+            scale((i + N - 1) % N, q);
+            part[q] = mma_fp8(cf[q], rf[i % NB]);
+            if (i == N - 1) {
+              __builtin_amdgcn_sched_barrier(0);  // the column fragment's registers are free from here on
+              if (more) cols(next, q);
+            }
+          }
           done = mine;
           __builtin_amdgcn_sched_barrier(0);  // or fragments are read far ahead, into registers that spill
         }
@@ -278,10 +282,12 @@ __global__ __launch_bounds__(WM* WN * 64) void k_tile_product(ProductArgs a, int
       int kb = 0;
       for (; kb + S < full; ++kb) step(kb, std::true_type{});
       for (; kb < steps; ++kb) step(kb, std::false_type{});
-      scale(N - 1, 1);
+#pragma unroll
+      for (int q = 0; q < TC; ++q) scale(N - 1, q);
     } else {
-      constexpr int N = 2 * NI;  // groups of 2 row fragments in a step: NI for each half of its inputs
-      u32x4_t cf[2][TC], rf[2][2];
+      constexpr int N = 2 * NI;           // groups of 2 row fragments in a step: NI for each half of its inputs
+      constexpr int NB = N == 4 ? 4 : 3;  // their buffers: group 0's is free when the last is multiplied
+      u32x4_t cf[2][TC], rf[NB][2];
       auto cols = [&](const char* st, auto h_) {
         constexpr int H = decltype(h_)::value;
         if constexpr (CT) {
@@ -296,7 +302,7 @@ __global__ __launch_bounds__(WM* WN * 64) void k_tile_product(ProductArgs a, int
       };
       auto rows = [&](const char* st, int it) {
 #pragma unroll
-        for (int v = 0; v < 2; ++v) rf[it & 1][v] = lds16(st + ra[it / NI] + ((it % NI) * 2 + v) * RSTEP);
+        for (int v = 0; v < 2; ++v) rf[it % NB][v] = lds16(st + ra[it / NI] + ((it % NI) * 2 + v) * RSTEP);
       };
       const std::integral_constant<int, 0> first;
       const std::integral_constant<int, 1> second;
@@ -305,32 +311,42 @@ __global__ __launch_bounds__(WM* WN * 64) void k_tile_product(ProductArgs a, int
         cols(smem, first);
         rows(smem, 0);
       }
-      // INNER: the step to be issued is whole, so that nothing branches
       auto step = [&](int kb, auto inner_) {
         constexpr bool INNER = decltype(inner_)::value;
+        const bool more = INNER || kb + 1 < steps;
         const char* st = stage_of(kb);
+        const char* next = stage_of(kb + 1);
+        rows(st, 1);
+        if (N > 2) rows(st, 2);
+        if (N == 2) cols(st, second);
 #pragma unroll
         for (int it = 0; it < N; ++it) {
-          if (it + 1 < N) {
-            if (it + 1 == NI) cols(st, second);
-            rows(st, it + 1);
-          } else if (INNER || kb + 1 < steps) {
+          if (N > 2 && it + 1 == NI) cols(st, second);
+          if (it > 0 && it + 2 < N) rows(st, it + 2);
+          // the stage's last reads are under way: the last two groups are
+          // multiplied behind the barrier, while the next stage's first
+          // fragments are read
+          if (it == N - 2 && more) {
             if constexpr (INNER) {
               barrier_keep<(S - 2) * LOADS>();
               issue_full(kb + S);
             } else {
               arrive(kb + 1);
             }
-            cols(stage_of(kb + 1), first);
-            rows(stage_of(kb + 1), 0);
+            if (N > 2 && !CT) cols(next, first);
+          }
+          if (it == N - 1 && more) {
+            if (N == 2 || CT) cols(next, first);
+            rows(next, 0);
           }
 #pragma unroll
           for (int v = 0; v < 2; ++v)
 #pragma unroll
             for (int q = 0; q < TC; ++q) {
               f32x4_t& c = acc[(it % NI) * 2 + v][q];
-              c = mma16<TYPE>(cf[it / NI][q], rf[it & 1][v], c);
+              c = mma16<TYPE>(cf[it / NI][q], rf[it % NB][v], c);
             }
+          __builtin_amdgcn_sched_barrier(0);
         }
       };
       int kb = 0;
