@@ -6,6 +6,7 @@ happens in libqsmoe.so's HIP kernels (argument marshalling here, nothing else).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from dataclasses import dataclass
 from typing import Optional
@@ -341,10 +342,21 @@ def forward_staged(layer: DeviceLayer, x: torch.Tensor, token_ids: Optional[torc
 
 
 # -- block-scaled FP8 and products grouped by expert ---------------------------
+#
+# The smallest of these calls take a few microseconds on the GPU, so what the
+# host spends per call shows: arguments go to ctypes as plain integers, and the
+# current stream's handle is asked for directly (0.06 us; a Stream object takes
+# 2.6 us of the 11 a call used to take).
 
 _DT = {torch.bfloat16: _lib.MOE_DT["bf16"], torch.float32: _lib.MOE_DT["f32"], torch.float16: _lib.MOE_DT["f16"]}
 _TORCH_DT = {"bf16": torch.bfloat16, "f32": torch.float32, "f16": torch.float16}
-_FP8 = (torch.float8_e4m3fn, torch.uint8)
+_E4M3 = torch.float8_e4m3fn
+_FP8 = (_E4M3, torch.uint8)
+_B16 = (torch.bfloat16, torch.float16)
+_F32 = (torch.float32,)
+_I32 = (torch.int32,)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _operand(t: torch.Tensor, name: str, dtypes, dims, device=None) -> torch.Tensor:
@@ -358,31 +370,37 @@ def _operand(t: torch.Tensor, name: str, dtypes, dims, device=None) -> torch.Ten
 
 
 def _shape(t: torch.Tensor, name: str, shape) -> None:
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _launch(device: torch.device, stream, body):
-    """body(raw stream) with `device` current and, if a stream is given, that
-    stream current too, so that what body allocates belongs to the stream its
-    kernels run on."""
-    if stream is None and device.index == torch.cuda.current_device():
-        return body(torch.cuda.current_stream().cuda_stream)
+def _elsewhere(device: torch.device, stream) -> bool:
+    """Whether a call has to make another device or stream current first."""
+    return stream is not None or device.index != torch.cuda.current_device()
+
+
+@contextlib.contextmanager
+def _on(device: torch.device, stream):
+    """`device` current and, if a stream is given, that stream too, so that what
+    a call allocates belongs to the stream its kernels run on."""
     with torch.cuda.device(device), torch.cuda.stream(stream):
-        return body(torch.cuda.current_stream().cuda_stream)
+        yield
 
 
 def _err_ptr(err: Optional[torch.Tensor], device) -> Optional[int]:
-    if err is None:
-        return None
-    return _operand(err, "err", (torch.int32,), (1,), device).data_ptr()
+    return None if err is None else _operand(err, "err", _I32, (1,), device).data_ptr()
+
+
+def _out_type(name: str) -> torch.dtype:
+    if name not in _TORCH_DT:
+        raise ValueError(f"output type must be one of {', '.join(_TORCH_DT)}, got {name!r}")
+    return _TORCH_DT[name]
 
 
 def _out(out: Optional[torch.Tensor], shape, dtype: torch.dtype, device) -> torch.Tensor:
     if out is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    _operand(out, "out", (torch.bfloat16, torch.float16, torch.float32), (len(shape),), device)
-    _shape(out, "out", shape)
+    _shape(_operand(out, "out", tuple(_DT), (len(shape),), device), "out", shape)
     return out
 
 
@@ -395,38 +413,36 @@ def quantize_block(x: torch.Tensor, block_rows: int = 1, pow2: bool = False, err
     """E4M3 codes with an fp32 scale per block of `block_rows` (1 or 128) rows
     and 128 columns (moe_quantize_block): x bf16, fp16 or fp32 [rows][cols], or
     [matrices][rows][cols] -> (codes float8_e4m3fn of x's shape, scales)."""
-    x = _operand(x, "x", tuple(_DT), (2, 3))
+    dev = _operand(x, "x", _DT, (2, 3)).device
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return quantize_block(x, block_rows, pow2, err)
     *lead, rows, cols = x.shape
-    n = lead[0] if lead else 1
-
-    def body(s):
-        codes = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
-        scales = torch.empty((*lead, -(-rows // max(block_rows, 1)), _blocks(cols)), dtype=torch.float32,
-                             device=x.device)
-        check(_lib.load().moe_quantize_block(x.data_ptr(), _DT[x.dtype], n, rows, cols, block_rows, int(pow2),
-                                             codes.data_ptr(), scales.data_ptr(), _err_ptr(err, x.device), s),
-              "moe_quantize_block")
-        return codes, scales
-    return _launch(x.device, stream, body)
+    codes = torch.empty_like(x, dtype=_E4M3)
+    scales = torch.empty((*lead, -(-rows // max(block_rows, 1)), _blocks(cols)), dtype=torch.float32, device=dev)
+    check(_lib.load().moe_quantize_block(x.data_ptr(), _DT[x.dtype], lead[0] if lead else 1, rows, cols, block_rows,
+                                         1 if pow2 else 0, codes.data_ptr(), scales.data_ptr(), _err_ptr(err, dev),
+                                         _raw_stream(dev.index)), "moe_quantize_block")
+    return codes, scales
 
 
 def swiglu_quantize_block(gu: torch.Tensor, pow2: bool = False, err: Optional[torch.Tensor] = None, stream=None):
     """silu(gate) * up of gu [rows][gate | up], quantised per 1 x 128 block
     (moe_swiglu_quantize_block) -> (codes [rows][inner], scales)."""
-    gu = _operand(gu, "gu", tuple(_DT), (2,))
+    dev = _operand(gu, "gu", _DT, (2,)).device
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return swiglu_quantize_block(gu, pow2, err)
     rows, two = gu.shape
     if two % 2:
         raise ValueError("gu must hold gate and up columns in equal number")
     inner = two // 2
-
-    def body(s):
-        codes = torch.empty((rows, inner), dtype=torch.float8_e4m3fn, device=gu.device)
-        scales = torch.empty((rows, _blocks(inner)), dtype=torch.float32, device=gu.device)
-        check(_lib.load().moe_swiglu_quantize_block(gu.data_ptr(), _DT[gu.dtype], rows, inner, int(pow2),
-                                                    codes.data_ptr(), scales.data_ptr(), _err_ptr(err, gu.device),
-                                                    s), "moe_swiglu_quantize_block")
-        return codes, scales
-    return _launch(gu.device, stream, body)
+    codes = torch.empty((rows, inner), dtype=_E4M3, device=dev)
+    scales = torch.empty((rows, _blocks(inner)), dtype=torch.float32, device=dev)
+    check(_lib.load().moe_swiglu_quantize_block(gu.data_ptr(), _DT[gu.dtype], rows, inner, 1 if pow2 else 0,
+                                                codes.data_ptr(), scales.data_ptr(), _err_ptr(err, dev),
+                                                _raw_stream(dev.index)), "moe_swiglu_quantize_block")
+    return codes, scales
 
 
 def matmul_block(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scales: torch.Tensor,
@@ -434,20 +450,19 @@ def matmul_block(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_sca
     """a @ b^T of block-scaled FP8 matrices (moe_matmul_block): a [M][K] with
     1 x 128 scales, b [N][K] with 128 x 128 scales -> [M][N]. A given `out`
     decides the output type."""
-    a = _operand(a, "a", _FP8, (2,))
-    dev = a.device
-    _operand(b, "b", _FP8, (2,), dev)
-    (M, K), N = a.shape, b.shape[0]
+    dev = _operand(a, "a", _FP8, (2,)).device
+    M, K = a.shape
+    N = _operand(b, "b", _FP8, (2,), dev).shape[0]
     _shape(b, "b", (N, K))
-    _shape(_operand(a_scales, "a_scales", (torch.float32,), (2,), dev), "a_scales", (M, _blocks(K)))
-    _shape(_operand(b_scales, "b_scales", (torch.float32,), (2,), dev), "b_scales", (_blocks(N), _blocks(K)))
-
-    def body(s):
-        y = _out(out, (M, N), _TORCH_DT[out_dtype], dev)
-        check(_lib.load().moe_matmul_block(a.data_ptr(), a_scales.data_ptr(), b.data_ptr(), b_scales.data_ptr(), M, N,
-                                           K, _DT[y.dtype], y.data_ptr(), s), "moe_matmul_block")
-        return y
-    return _launch(dev, stream, body)
+    _shape(_operand(a_scales, "a_scales", _F32, (2,), dev), "a_scales", (M, _blocks(K)))
+    _shape(_operand(b_scales, "b_scales", _F32, (2,), dev), "b_scales", (_blocks(N), _blocks(K)))
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return matmul_block(a, a_scales, b, b_scales, out_dtype, out)
+    y = _out(out, (M, N), _out_type(out_dtype), dev)
+    check(_lib.load().moe_matmul_block(a.data_ptr(), a_scales.data_ptr(), b.data_ptr(), b_scales.data_ptr(), M, N, K,
+                                       _DT[y.dtype], y.data_ptr(), _raw_stream(dev.index)), "moe_matmul_block")
+    return y
 
 
 def _groups(rows: int, order: str, top_k: int, offsets: torch.Tensor, perm: Optional[torch.Tensor], E: int, dev):
@@ -459,9 +474,9 @@ def _groups(rows: int, order: str, top_k: int, offsets: torch.Tensor, perm: Opti
     if order != "token" and rows % top_k:
         raise ValueError(f"{rows} rows in {order} order are no multiple of top_k = {top_k}")
     T = rows if order == "token" else rows // top_k
-    _shape(_operand(offsets, "offsets", (torch.int32,), (1,), dev), "offsets", (E + 1,))
+    _shape(_operand(offsets, "offsets", _I32, (1,), dev), "offsets", (E + 1,))
     if perm is not None:
-        _shape(_operand(perm, "perm", (torch.int32,), (1,), dev), "perm", (T * top_k,))
+        _shape(_operand(perm, "perm", _I32, (1,), dev), "perm", (T * top_k,))
     return T
 
 
@@ -475,23 +490,23 @@ def grouped_matmul_block(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tenso
     ("bucket", "token" or "slot"), w [E][N][K] with 128 x 128 scales, offsets
     and perm as `permute` gives them -> [T * top_k][N] in `out_order` ("bucket"
     or "slot"). Rows of no bucket are not written."""
-    a = _operand(a, "a", _FP8, (2,))
-    dev = a.device
+    dev = _operand(a, "a", _FP8, (2,)).device
     E, N, K = _operand(w, "w", _FP8, (3,), dev).shape
-    _shape(a, "a", (a.shape[0], K))
-    _shape(_operand(a_scales, "a_scales", (torch.float32,), (2,), dev), "a_scales", (a.shape[0], _blocks(K)))
-    _shape(_operand(w_scales, "w_scales", (torch.float32,), (3,), dev), "w_scales", (E, _blocks(N), _blocks(K)))
-    T = _groups(a.shape[0], x_order, top_k, offsets, perm, E, dev)
-
-    def body(s):
-        y = _out(out, (T * top_k, N), _TORCH_DT[out_dtype], dev)
-        check(_lib.load().moe_grouped_matmul_block(
-            a.data_ptr(), a_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(), T, top_k, N, K, E,
-            offsets.data_ptr(), None if perm is None else perm.data_ptr(), _lib.MOE_ROWS[x_order],
-            _lib.MOE_ROWS.get(out_order, -1), _DT[y.dtype], y.data_ptr(), _err_ptr(err, dev), s),
-            "moe_grouped_matmul_block")
-        return y
-    return _launch(dev, stream, body)
+    rows = a.shape[0]
+    _shape(a, "a", (rows, K))
+    _shape(_operand(a_scales, "a_scales", _F32, (2,), dev), "a_scales", (rows, _blocks(K)))
+    _shape(_operand(w_scales, "w_scales", _F32, (3,), dev), "w_scales", (E, _blocks(N), _blocks(K)))
+    T = _groups(rows, x_order, top_k, offsets, perm, E, dev)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return grouped_matmul_block(a, a_scales, w, w_scales, offsets, perm, top_k, x_order, out_order, out_dtype,
+                                        out, err)
+    y = _out(out, (T * top_k, N), _out_type(out_dtype), dev)
+    check(_lib.load().moe_grouped_matmul_block(
+        a.data_ptr(), a_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(), T, top_k, N, K, E, offsets.data_ptr(),
+        None if perm is None else perm.data_ptr(), _lib.MOE_ROWS[x_order], _lib.MOE_ROWS.get(out_order, -1),
+        _DT[y.dtype], y.data_ptr(), _err_ptr(err, dev), _raw_stream(dev.index)), "moe_grouped_matmul_block")
+    return y
 
 
 def grouped_matmul(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, perm: Optional[torch.Tensor] = None,
@@ -503,20 +518,21 @@ def grouped_matmul(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, perm
     (the gradient in the rows of a product with w^T). Orders as in
     grouped_matmul_block; the output type is x's unless `out_dtype` or `out`
     says otherwise."""
-    x = _operand(x, "x", (torch.bfloat16, torch.float16), (2,))
-    dev = x.device
+    dev = _operand(x, "x", _B16, (2,)).device
     E, N, K = _operand(w, "w", (x.dtype,), (3,), dev).shape
-    _shape(x, "x", (x.shape[0], N if transposed else K))
-    T = _groups(x.shape[0], x_order, top_k, offsets, perm, E, dev)
-
-    def body(s):
-        y = _out(out, (T * top_k, K if transposed else N), x.dtype if out_dtype is None else _TORCH_DT[out_dtype], dev)
-        check(_lib.load().moe_grouped_matmul(
-            x.data_ptr(), w.data_ptr(), _DT[x.dtype], T, top_k, N, K, E, offsets.data_ptr(),
-            None if perm is None else perm.data_ptr(), _lib.MOE_ROWS[x_order], _lib.MOE_ROWS.get(out_order, -1),
-            int(transposed), _DT[y.dtype], y.data_ptr(), _err_ptr(err, dev), s), "moe_grouped_matmul")
-        return y
-    return _launch(dev, stream, body)
+    rows = x.shape[0]
+    _shape(x, "x", (rows, N if transposed else K))
+    T = _groups(rows, x_order, top_k, offsets, perm, E, dev)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return grouped_matmul(x, w, offsets, perm, top_k, x_order, out_order, transposed, out_dtype, out, err)
+    y = _out(out, (T * top_k, K if transposed else N), x.dtype if out_dtype is None else _out_type(out_dtype), dev)
+    check(_lib.load().moe_grouped_matmul(
+        x.data_ptr(), w.data_ptr(), _DT[x.dtype], T, top_k, N, K, E, offsets.data_ptr(),
+        None if perm is None else perm.data_ptr(), _lib.MOE_ROWS[x_order], _lib.MOE_ROWS.get(out_order, -1),
+        1 if transposed else 0, _DT[y.dtype], y.data_ptr(), _err_ptr(err, dev), _raw_stream(dev.index)),
+        "moe_grouped_matmul")
+    return y
 
 
 def grouped_matmul_dw(x: torch.Tensor, dy: torch.Tensor, offsets: torch.Tensor, perm: Optional[torch.Tensor] = None,
@@ -526,19 +542,18 @@ def grouped_matmul_dw(x: torch.Tensor, dy: torch.Tensor, offsets: torch.Tensor, 
     """The gradient of grouped_matmul in the weights (moe_grouped_matmul_dw):
     x [rows][K] in `x_order`, dy [T * top_k][N] in `dy_order` ("bucket" or
     "slot") -> [E][N][K], the sum over each expert's positions of dy x^T."""
-    x = _operand(x, "x", (torch.bfloat16, torch.float16), (2,))
-    dev = x.device
-    _operand(dy, "dy", (x.dtype,), (2,), dev)
+    dev = _operand(x, "x", _B16, (2,)).device
+    rows, K = x.shape
+    N = _operand(dy, "dy", (x.dtype,), (2,), dev).shape[1]
     E = offsets.shape[0] - 1 if offsets.dim() == 1 else 0
-    N, K = dy.shape[1], x.shape[1]
-    T = _groups(x.shape[0], x_order, top_k, offsets, perm, E, dev)
+    T = _groups(rows, x_order, top_k, offsets, perm, E, dev)
     _shape(dy, "dy", (T * top_k, N))
-
-    def body(s):
-        dw = _out(out, (E, N, K), _TORCH_DT[out_dtype], dev)
-        check(_lib.load().moe_grouped_matmul_dw(
-            x.data_ptr(), dy.data_ptr(), _DT[x.dtype], T, top_k, N, K, E, offsets.data_ptr(),
-            None if perm is None else perm.data_ptr(), _lib.MOE_ROWS[x_order], _lib.MOE_ROWS.get(dy_order, -1),
-            _DT[dw.dtype], dw.data_ptr(), _err_ptr(err, dev), s), "moe_grouped_matmul_dw")
-        return dw
-    return _launch(dev, stream, body)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return grouped_matmul_dw(x, dy, offsets, perm, top_k, x_order, dy_order, out_dtype, out, err)
+    dw = _out(out, (E, N, K), _out_type(out_dtype), dev)
+    check(_lib.load().moe_grouped_matmul_dw(
+        x.data_ptr(), dy.data_ptr(), _DT[x.dtype], T, top_k, N, K, E, offsets.data_ptr(),
+        None if perm is None else perm.data_ptr(), _lib.MOE_ROWS[x_order], _lib.MOE_ROWS.get(dy_order, -1),
+        _DT[dw.dtype], dw.data_ptr(), _err_ptr(err, dev), _raw_stream(dev.index)), "moe_grouped_matmul_dw")
+    return dw
