@@ -151,10 +151,23 @@ __device__ __forceinline__ void store8(char* p, int out_type, f32x4_t v, f32x4_t
   }
 }
 
+// Inclusive sum over the wave's lanes: rows of 16 by DPP shifts, then the row
+// totals handed on.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);  // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, true);  // row_bcast:15 into rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, true);  // row_bcast:31 into rows 2 and 3
+  return v;
+}
+
 // Tile `pair` of the list of every expert's (row tile, column tile) pairs.
-// Each wave finds it by itself: 64 experts' tile counts at a time, scanned
-// across the lanes. Within an expert row tiles run fastest, in bands of 8, so
-// that the workgroups of one XCD share both a band's rows and few column tiles.
+// Each wave finds it by itself, without LDS or a barrier: 4 experts a lane,
+// their tile counts scanned across the lanes, 256 experts at a time. Within an
+// expert row tiles run fastest, in bands of 8, so that the workgroups of one
+// XCD share both a band's rows and few column tiles.
 struct TileAt {
   int e, first, rows, ctile;
 };
@@ -165,26 +178,37 @@ __device__ __forceinline__ bool find_tile(const int32_t* offsets, int E, int n, 
   if (offsets) {
     const int lane = lane_id();
     bool found = false;
-    for (int e0 = 0; e0 < E; e0 += 64) {
-      const int i = e0 + lane;
-      const int a = i < E ? min(max(offsets[i], 0), n) : 0;
-      const int b = i < E ? min(max(offsets[i + 1], 0), n) : 0;
-      const int mt = (max(b - a, 0) + BM - 1) / BM;
-      int incl = mt;
+    for (int e0 = 0; e0 < E; e0 += 256) {
+      const int i = e0 + 4 * lane;
+      int o[5], mt[4];
 #pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int y = __shfl_up(incl, o);
-        if (lane >= o) incl += y;
+      for (int v = 0; v < 5; ++v) o[v] = min(max(offsets[min(i + v, E)], 0), n);
+      int sum = 0;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        mt[v] = (max(o[v + 1] - o[v], 0) + BM - 1) / BM;  // 0 past the last expert
+        sum += mt[v];
       }
-      const int64_t end = before + static_cast<int64_t>(incl) * ctiles;
-      const uint64_t m = __ballot(end > pair);
+      const int incl = wave_scan(sum);
+      const uint64_t m = __ballot(before + static_cast<int64_t>(incl) * ctiles > pair);
       if (m != 0) {
         const int src = __ffsll(static_cast<unsigned long long>(m)) - 1;
-        e = e0 + src;
-        lo = __builtin_amdgcn_readlane(a, src);
-        count = __builtin_amdgcn_readlane(b, src) - lo;
-        before += static_cast<int64_t>(__builtin_amdgcn_readlane(incl - mt, src)) * ctiles;
-        found = true;
+        before += static_cast<int64_t>(__builtin_amdgcn_readlane(incl - sum, src)) * ctiles;
+        e = e0 + 4 * src;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int64_t here = static_cast<int64_t>(__builtin_amdgcn_readlane(mt[v], src)) * ctiles;
+          if (!found) {
+            if (before + here > pair) {
+              found = true;
+              e += v;
+              lo = __builtin_amdgcn_readlane(o[v], src);
+              count = __builtin_amdgcn_readlane(o[v + 1], src) - lo;
+            } else {
+              before += here;
+            }
+          }
+        }
         break;
       }
       before += static_cast<int64_t>(__builtin_amdgcn_readlane(incl, 63)) * ctiles;

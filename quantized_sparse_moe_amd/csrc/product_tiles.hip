@@ -392,6 +392,128 @@ __global__ __launch_bounds__(WM* WN * 64) void k_tile_product(ProductArgs a, int
   }
 }
 
+// Few rows: what bounds the product is reading each weight once, and with few
+// tiles the latency of doing so. A workgroup takes 16 RT rows and 16 columns of
+// one expert and its 4 waves every fourth step of the contraction each, weights
+// and rows straight from memory into registers, a group of steps ahead; their
+// sums meet in LDS in a fixed order.
+template <int TYPE, int RT>
+__global__ __launch_bounds__(256) void k_split_product(ProductArgs a, int run) {
+  constexpr bool FP8 = TYPE == kTypeE4m3 || TYPE == kE4m3Wide;
+  constexpr int ESIZE = FP8 ? 1 : 2;
+  constexpr int BM = 16 * RT, BN = 16, W = 4;
+  constexpr int U = 4 / RT;  // steps of a group
+  __shared__ f32x4_t s_sum[W][RT][64];
+
+  const int n = a.T * a.k;
+  TileAt t;
+  if (!find_tile<BM>(a.offsets, a.E, n, (a.C + BN - 1) / BN, pair_of_block(run), &t)) return;
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, j = lane & 15;
+  const int c0 = t.ctile * BN;
+  const int qbytes = a.Q * ESIZE;
+  const int steps = (qbytes + kStepBytes - 1) / kStepBytes;
+  const int qb = (a.Q + 127) / 128;
+
+  // 32 bytes of a column's weights and of a row per lane and step
+  const char* wp = static_cast<const char*>(a.c) +
+                   (static_cast<int64_t>(t.e) * a.C + min(c0 + j, a.C - 1)) * qbytes + 32 * g;
+  const char* rp[RT];
+  const float* rs[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    const int row = max(row_of(a.perm, a.r_order, a.k, n, t.first + min(16 * i + j, t.rows - 1), a.err), 0);
+    rp[i] = static_cast<const char*>(a.r) + static_cast<int64_t>(row) * qbytes + 32 * g;
+    rs[i] = FP8 ? a.r_scales + static_cast<int64_t>(row) * qb : nullptr;
+  }
+  const float* cs = FP8 ? a.c_scales + (static_cast<int64_t>(t.e) * ((a.C + 127) / 128) + c0 / 128) * qb : nullptr;
+
+  struct Group {
+    u32x4_t w[U][2], r[U][RT][2];
+    float s[U][RT];
+  };
+  auto load = [&](int i, Group& f) {  // the wave's steps 4 i U, ...
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int kb = (i * U + u) * W + wave;
+      const int rest = qbytes - kb * kStepBytes - 32 * g;  // this lane's bytes from here on
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        f.w[u][h] = u32x4_t{0, 0, 0, 0};
+        if (16 * h < rest) f.w[u][h] = *reinterpret_cast<const u32x4_t*>(wp + kb * kStepBytes + 16 * h);
+#pragma unroll
+        for (int v = 0; v < RT; ++v) {
+          f.r[u][v][h] = u32x4_t{0, 0, 0, 0};
+          if (16 * h < rest) f.r[u][v][h] = *reinterpret_cast<const u32x4_t*>(rp[v] + kb * kStepBytes + 16 * h);
+        }
+      }
+      if constexpr (FP8) {
+        const int b = min(kb, qb - 1);
+#pragma unroll
+        for (int v = 0; v < RT; ++v) f.s[u][v] = rs[v][b] * cs[b];
+      }
+    }
+  };
+  f32x4_t acc[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) acc[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  auto multiply = [&](int i, const Group& f) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if ((i * U + u) * W + wave >= steps) continue;
+#pragma unroll
+      for (int v = 0; v < RT; ++v) {
+        if constexpr (FP8) {
+          f32x4_t part = {0.0f, 0.0f, 0.0f, 0.0f};
+          if constexpr (TYPE == kE4m3Wide) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int x = 0; x < 4; x += 2)
+                part = mma16<0>(e4m3_to_bf16x8(f.w[u][h][x], f.w[u][h][x + 1]),
+                                e4m3_to_bf16x8(f.r[u][v][h][x], f.r[u][v][h][x + 1]), part);
+          } else {
+            part = mma_fp8(
+                __builtin_bit_cast(i32x8_t, __builtin_shufflevector(f.w[u][0], f.w[u][1], 0, 1, 2, 3, 4, 5, 6, 7)),
+                __builtin_bit_cast(i32x8_t, __builtin_shufflevector(f.r[u][v][0], f.r[u][v][1], 0, 1, 2, 3, 4, 5, 6, 7)));
+          }
+#pragma unroll
+          for (int x = 0; x < 4; ++x) acc[v][x] = fmaf(part[x], f.s[u][v], acc[v][x]);
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) acc[v] = mma16<TYPE>(f.w[u][h], f.r[u][v][h], acc[v]);
+        }
+      }
+    }
+  };
+
+  const int groups = (steps + W * U - 1) / (W * U);
+  Group f[2];
+  if (groups > 0) load(0, f[0]);
+  for (int i = 0; i < groups; i += 2) {
+    if (i + 1 < groups) load(i + 1, f[1]);
+    multiply(i, f[0]);
+    if (i + 1 < groups) {
+      if (i + 2 < groups) load(i + 2, f[0]);
+      multiply(i + 1, f[1]);
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < RT; ++v) s_sum[wave][v][lane] = acc[v];
+  __syncthreads();
+  for (int v = wave; v < RT; v += W) {
+    f32x4_t sum = s_sum[0][v][lane];
+#pragma unroll
+    for (int w = 1; w < W; ++w) sum += s_sum[w][v][lane];
+    const int r = 16 * v + j, c = c0 + 4 * g;
+    if (r >= t.rows || c >= a.C) continue;
+    const int row = row_of(a.perm, a.out_order, a.k, n, t.first + r, a.err);
+    if (row < 0) continue;
+    store4(static_cast<char*>(a.out) + (static_cast<int64_t>(row) * a.C + c) * (a.out_type == 1 ? 4 : 2), a.out_type,
+           sum);
+  }
+}
+
 // The gradient in the weights: rows are dy's columns n, columns x's columns k,
 // and the contraction runs over the expert's positions, 32 at a time; both
 // operands are stored across it. A bucket is short against the tile (12 steps
@@ -602,10 +724,30 @@ hipError_t launch_tiles(const ProductArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <int TYPE, int RT>
+hipError_t launch_split(const ProductArgs& a, hipStream_t s) {
+  const int64_t n = static_cast<int64_t>(a.T) * a.k;
+  const int64_t pairs =
+      (a.offsets ? n / (16 * RT) + std::min<int64_t>(a.E, n) : (n + 16 * RT - 1) / (16 * RT)) * ((a.C + 15) / 16);
+  const int run = static_cast<int>(std::min<int64_t>(32, (pairs + 7) / 8));
+  const int64_t grid = (pairs + 8 * run - 1) / (8 * run) * (8 * run);
+  if (grid > INT32_MAX) return hipErrorInvalidValue;
+  QSMOE_LAUNCH((k_split_product<TYPE, RT>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, a, run);
+  return hipGetLastError();
+}
+
 template <int TYPE, bool CT>
 hipError_t pick_tiles(const ProductArgs& a, hipStream_t s) {
   const int64_t n = static_cast<int64_t>(a.T) * a.k;
   const int64_t mean = n / a.E;
+  if constexpr (!CT) {
+    const int64_t tiles = (n / 64 + std::min<int64_t>(a.E, n)) * ((a.C + 127) / 128);
+    if (tiles <= 256) {
+      if (mean <= 16) return launch_split<TYPE, 1>(a, s);
+      if (mean <= 32) return launch_split<TYPE, 2>(a, s);
+      return launch_split<TYPE, 4>(a, s);
+    }
+  }
   if constexpr (TYPE != kE4m3Wide)
     if (mean >= 192) return launch_tiles<TYPE, 256, 256, 2, 4, 2, CT>(a, s);
   if (mean >= 48) return launch_tiles<TYPE, 128, 256, 2, 4, 3, CT>(a, s);
