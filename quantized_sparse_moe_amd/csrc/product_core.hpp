@@ -18,16 +18,19 @@ typedef __attribute__((address_space(3))) u32x4_t lds_u32x4_t;
 
 enum : int { kBucket = 0, kToken = 1, kSlot = 2 };  // moe_rows
 
-// The row of a matrix in `order` that belongs to bucket position p, or -1
-// where perm holds no assignment (which sets the error bit).
-__device__ __forceinline__ int row_of(const int32_t* perm, int order, int k, int n, int p, int32_t* err) {
-  if (order == kBucket) return p;
-  const int a = perm[p];
+// The row of a matrix in `order` that belongs to a bucket position, from the
+// position (bucket order) or perm's entry for it; -1 where perm holds no
+// assignment (which sets the error bit).
+__device__ __forceinline__ int row_in(int a, int order, int k, int n, int32_t* err) {
+  if (order == kBucket) return a;
   if (a < 0 || a >= n) {
     set_device_error(err, 16);
     return -1;
   }
   return order == kToken ? a / k : a;
+}
+__device__ __forceinline__ int row_of(const int32_t* perm, int order, int k, int n, int p, int32_t* err) {
+  return row_in(order == kBucket ? p : perm[p], order, k, n, err);
 }
 
 // Direct global -> LDS load of 16 bytes per lane: lane l's bytes land at

@@ -740,17 +740,38 @@ template <int TYPE, bool CT>
 hipError_t pick_tiles(const ProductArgs& a, hipStream_t s) {
   const int64_t n = static_cast<int64_t>(a.T) * a.k;
   const int64_t mean = n / a.E;
+  // Row tiles of height h: exact without groups, else every bucket's last one
+  // taken as half full (a bucket of fewer rows than h still takes one).
+  const int64_t used = std::min<int64_t>(a.E, n);
+  auto tiles = [&](int h, int w) {
+    const int64_t m = a.offsets ? std::max<int64_t>(used, n / h + used / 2) : (n + h - 1) / h;
+    return m * ((a.C + w - 1) / w);
+  };
+  // What a tile size gives was measured on dense FP8 products of 4096 x 4096
+  // weights: 256 x 256 0.97 ms per 10^12 products where it fills the chip
+  // (128 x 256: 1.2, 128 x 128: 1.3, 64 x 128: 1.6), but one round of tiles
+  // takes 59 / 40 / 30 / 19 us however few they are (the last two two to a
+  // CU: 47 / 31 us when doubled). So: the largest size whose tiles fill most
+  // of the 256 CUs, and for buckets only while rows fill the tile; a grouped
+  // product in few rounds of 128 x 256 tiles takes the 128 x 128 ones, which
+  // ragged buckets spread better (fp16, 24 buckets of 84 rows: 39 against
+  // 55 us).
   if constexpr (!CT) {
-    const int64_t tiles = (n / 64 + std::min<int64_t>(a.E, n)) * ((a.C + 127) / 128);
-    if (tiles <= 256) {
+    // 16 columns of split contraction: 64 rows of 4096 x 4096 16 us against
+    // 19, 128 rows 28 against 19; one row 7.4 against 17
+    if (tiles(64, 128) <= 256) {
       if (mean <= 16) return launch_split<TYPE, 1>(a, s);
       if (mean <= 32) return launch_split<TYPE, 2>(a, s);
-      return launch_split<TYPE, 4>(a, s);
+      if (mean <= 64 && tiles(64, 128) <= 32) return launch_split<TYPE, 4>(a, s);
     }
   }
-  if constexpr (TYPE != kE4m3Wide)
-    if (mean >= 192) return launch_tiles<TYPE, 256, 256, 2, 4, 2, CT>(a, s);
-  if (mean >= 48) return launch_tiles<TYPE, 128, 256, 2, 4, 3, CT>(a, s);
+  if constexpr (TYPE != kE4m3Wide) {
+    if (mean >= 192 && tiles(256, 256) >= 192) return launch_tiles<TYPE, 256, 256, 2, 4, 2, CT>(a, s);
+  }
+  if (mean >= 48) {
+    if (tiles(128, 256) >= (a.offsets ? 512 : 192)) return launch_tiles<TYPE, 128, 256, 2, 4, 3, CT>(a, s);
+    if (tiles(128, 128) >= 256) return launch_tiles<TYPE, 128, 128, 2, 2, 2, CT>(a, s);
+  }
   return launch_tiles<TYPE, 64, 128, 2, 2, 3, CT>(a, s);
 }
 
