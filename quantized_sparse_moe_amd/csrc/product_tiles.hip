@@ -547,22 +547,27 @@ __global__ __launch_bounds__(256, 2) void k_tile_dw(DwArgs a, int64_t pairs, int
   const int g = lane >> 4, j = lane & 15;
   const int steps = (count + BK - 1) / BK, full = count / BK;
 
-  // this thread's pieces: contraction rows rq + i * NT / RPR and columns
+  // This thread's pieces: contraction rows rq + i * NT / RPR (cq ...), at byte
+  // offsets rcol (ccol) of a row. In bucket order a step's rows follow each
+  // other, so that the offsets from the step's first row never change; else
+  // each row is looked up a step ahead.
   const int rq = tid / RPR, cq = tid / CPR;
-  int rcol[NR], ccol[NC];
+  const uint32_t rld = a.N * 2, cld = a.K * 2;  // bytes of a row
+  uint32_t rcol[NR], ccol[NC];
 #pragma unroll
   for (int i = 0; i < NR; ++i) {
     const int col = r0 + ((tid % RPR) ^ swz_q(rq + i * (NT / RPR))) * 8;
-    rcol[i] = col < a.N ? col : r0;
+    rcol[i] = (col < a.N ? col : r0) * 2;
+    if (a.dy_order == kBucket) rcol[i] += (rq + i * (NT / RPR)) * rld;
   }
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int col = c0 + ((tid % CPR) ^ swz_q(cq + i * (NT / CPR))) * 8;
-    ccol[i] = col < a.K ? col : c0;
+    ccol[i] = (col < a.K ? col : c0) * 2;
+    if (a.x_order == kBucket) ccol[i] += (cq + i * (NT / CPR)) * cld;
   }
-  // perm's entries of the step to be issued next
   const double per_k = 1.0 / a.k;  // (a + 1/2) / k in 64 bits floors right for every a < 2^31
-  int rraw[NR], craw[NC];
+  int rraw[NR], craw[NC];          // perm's entries of the step to be issued next
   auto look_up = [&](int kb) {
     if (kb >= steps) return;
     if (a.dy_order != kBucket) {
@@ -574,47 +579,60 @@ __global__ __launch_bounds__(256, 2) void k_tile_dw(DwArgs a, int64_t pairs, int
       for (int i = 0; i < NC; ++i) craw[i] = a.perm[lo + min(kb * BK + cq + i * (NT / CPR), count - 1)];
     }
   };
-  auto row = [&](int raw, int order, int p) {
-    if (order == kBucket) return p;
-    if (raw < 0 || raw >= n) {
+  auto row = [&](int raw, int order) -> uint32_t {
+    if (static_cast<uint32_t>(raw) >= static_cast<uint32_t>(n)) {
       set_device_error(a.err, 16);
       raw = 0;
     }
-    return order == kToken ? static_cast<int>((raw + 0.5) * per_k) : raw;
+    return order == kToken ? static_cast<uint32_t>((raw + 0.5) * per_k) : raw;
   };
-  // Issue step kb, and look up the rows of the step after it before that, so
-  // that waiting for them does not wait for this step's data.
+  // Issue step kb. The next step's rows are looked up before its data, so that
+  // waiting for them does not wait for the data.
   auto issue = [&](int kb) {
     char* sr = smem + (kb % S) * STAGE + wave * 1024;
     char* sc = sr + RB;
-    const uint16_t* dy = static_cast<const uint16_t*>(a.dy);
-    const uint16_t* x = static_cast<const uint16_t*>(a.x);
-    int rr[NR], cr[NC];
+    const char* dy = static_cast<const char*>(a.dy);
+    const char* x = static_cast<const char*>(a.x);
+    uint64_t rr[NR], cr[NC];
+    if (a.dy_order != kBucket) {
 #pragma unroll
-    for (int i = 0; i < NR; ++i)
-      rr[i] = row(rraw[i], a.dy_order, lo + min(kb * BK + rq + i * (NT / RPR), count - 1));
+      for (int i = 0; i < NR; ++i) rr[i] = static_cast<uint64_t>(row(rraw[i], a.dy_order)) * rld + rcol[i];
+    }
+    if (a.x_order != kBucket) {
 #pragma unroll
-    for (int i = 0; i < NC; ++i)
-      cr[i] = row(craw[i], a.x_order, lo + min(kb * BK + cq + i * (NT / CPR), count - 1));
+      for (int i = 0; i < NC; ++i) cr[i] = static_cast<uint64_t>(row(craw[i], a.x_order)) * cld + ccol[i];
+    }
     look_up(kb + 1);
+    const char* dy0 = dy + static_cast<int64_t>(lo + kb * BK) * rld;
+    const char* x0 = x + static_cast<int64_t>(lo + kb * BK) * cld;
     if (kb < full) {
+      if (a.dy_order == kBucket) {
 #pragma unroll
-      for (int i = 0; i < NR; ++i) load_lds16(dy + static_cast<int64_t>(rr[i]) * a.N + rcol[i], sr + i * NT * 16);
+        for (int i = 0; i < NR; ++i) load_lds16(dy0 + rcol[i], sr + i * NT * 16);
+      } else {
 #pragma unroll
-      for (int i = 0; i < NC; ++i) load_lds16(x + static_cast<int64_t>(cr[i]) * a.K + ccol[i], sc + i * NT * 16);
+        for (int i = 0; i < NR; ++i) load_lds16(dy + rr[i], sr + i * NT * 16);
+      }
+      if (a.x_order == kBucket) {
+#pragma unroll
+        for (int i = 0; i < NC; ++i) load_lds16(x0 + ccol[i], sc + i * NT * 16);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NC; ++i) load_lds16(x + cr[i], sc + i * NT * 16);
+      }
     } else {  // zeros behind the bucket's end
       const u32x4_t zero = {0, 0, 0, 0};
 #pragma unroll
       for (int i = 0; i < NR; ++i) {
         if (kb * BK + rq + i * (NT / RPR) < count)
-          load_lds16(dy + static_cast<int64_t>(rr[i]) * a.N + rcol[i], sr + i * NT * 16);
+          load_lds16(a.dy_order == kBucket ? dy0 + rcol[i] : dy + rr[i], sr + i * NT * 16);
         else
           *reinterpret_cast<u32x4_t*>(sr + i * NT * 16 + lane * 16) = zero;
       }
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         if (kb * BK + cq + i * (NT / CPR) < count)
-          load_lds16(x + static_cast<int64_t>(cr[i]) * a.K + ccol[i], sc + i * NT * 16);
+          load_lds16(a.x_order == kBucket ? x0 + ccol[i] : x + cr[i], sc + i * NT * 16);
         else
           *reinterpret_cast<u32x4_t*>(sc + i * NT * 16 + lane * 16) = zero;
       }
