@@ -440,8 +440,8 @@ moe_status moe_matmul_block(const uint8_t* a, const float* a_scales, const uint8
  * neither read nor written, so their output rows stay as they were. Offsets
  * are clamped to [0, T*k], and buckets that do not ascend count as empty. A
  * perm entry outside [0, T*k) sets MOE_DEVERR_ROW_INDEX in *err (device int32
- * or NULL); row 0 is read in its place, and an output row that it would name
- * is not written. perm may be NULL when no matrix is in token or slot order;
+ * or NULL); some row of the matrix is read in its place, and an output row that
+ * it would name is not written. perm may be NULL when no matrix is in token or slot order;
  * it must not name an output row twice.
  *
  * moe_grouped_matmul_block: out[p][n] = sum_k a[p][k] * w[e(p)][n][k] over

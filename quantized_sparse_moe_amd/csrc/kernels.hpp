@@ -178,6 +178,7 @@ struct DwArgs {
   int32_t x_order, dy_order;
   void* out;
   int32_t* err;
+  uint32_t k_magic = 0, k_shift = 0;  // division of x's row by k, set by the launcher
 };
 hipError_t launch_product_dw(const DwArgs& a, hipStream_t s);
 

@@ -520,7 +520,7 @@ __global__ __launch_bounds__(256) void k_split_product(ProductArgs a, int run) {
 // of 64 for 768 rows), so what precedes and follows the steps counts: two
 // workgroups share a CU (24 KB a stage, at most 256 registers a wave), and one
 // stores its 128 KB of fp32 results while the other multiplies.
-template <int TYPE, int BM, int BN>
+template <int TYPE, int BM, int BN, bool LOOKUP>
 __global__ __launch_bounds__(256, 2) void k_tile_dw(DwArgs a, int64_t pairs, int run) {
   constexpr int S = 3, BK = 32, NT = 256, WM = 2, WN = 2;
   constexpr int TR = BM / WM / 16, TC = BN / WN / 16;
@@ -550,89 +550,86 @@ __global__ __launch_bounds__(256, 2) void k_tile_dw(DwArgs a, int64_t pairs, int
   // This thread's pieces: contraction rows rq + i * NT / RPR (cq ...), at byte
   // offsets rcol (ccol) of a row. In bucket order a step's rows follow each
   // other, so that the offsets from the step's first row never change; else
-  // each row is looked up a step ahead.
+  // (LOOKUP) each row is looked up a step ahead.
   const int rq = tid / RPR, cq = tid / CPR;
   const uint32_t rld = a.N * 2, cld = a.K * 2;  // bytes of a row
   uint32_t rcol[NR], ccol[NC];
 #pragma unroll
   for (int i = 0; i < NR; ++i) {
     const int col = r0 + ((tid % RPR) ^ swz_q(rq + i * (NT / RPR))) * 8;
-    rcol[i] = (col < a.N ? col : r0) * 2;
-    if (a.dy_order == kBucket) rcol[i] += (rq + i * (NT / RPR)) * rld;
+    rcol[i] = (col < a.N ? col : r0) * 2 + (LOOKUP ? 0 : (rq + i * (NT / RPR)) * rld);
   }
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int col = c0 + ((tid % CPR) ^ swz_q(cq + i * (NT / CPR))) * 8;
-    ccol[i] = (col < a.K ? col : c0) * 2;
-    if (a.x_order == kBucket) ccol[i] += (cq + i * (NT / CPR)) * cld;
+    ccol[i] = (col < a.K ? col : c0) * 2 + (LOOKUP ? 0 : (cq + i * (NT / CPR)) * cld);
   }
-  const double per_k = 1.0 / a.k;  // (a + 1/2) / k in 64 bits floors right for every a < 2^31
-  int rraw[NR], craw[NC];          // perm's entries of the step to be issued next
+  int rraw[NR], craw[NC];  // perm's entries of the step to be issued next
+  auto rpos = [&](int kb, int i) { return lo + min(kb * BK + rq + i * (NT / RPR), count - 1); };
+  auto cpos = [&](int kb, int i) { return lo + min(kb * BK + cq + i * (NT / CPR), count - 1); };
   auto look_up = [&](int kb) {
-    if (kb >= steps) return;
-    if (a.dy_order != kBucket) {
+    if constexpr (LOOKUP) {
 #pragma unroll
-      for (int i = 0; i < NR; ++i) rraw[i] = a.perm[lo + min(kb * BK + rq + i * (NT / RPR), count - 1)];
-    }
-    if (a.x_order != kBucket) {
+      for (int i = 0; i < NR; ++i) rraw[i] = a.perm[rpos(kb, i)];
 #pragma unroll
-      for (int i = 0; i < NC; ++i) craw[i] = a.perm[lo + min(kb * BK + cq + i * (NT / CPR), count - 1)];
+      for (int i = 0; i < NC; ++i) craw[i] = a.perm[cpos(kb, i)];
     }
   };
-  auto row = [&](int raw, int order) -> uint32_t {
-    if (static_cast<uint32_t>(raw) >= static_cast<uint32_t>(n)) {
-      set_device_error(a.err, 16);
-      raw = 0;
-    }
-    return order == kToken ? static_cast<uint32_t>((raw + 0.5) * per_k) : raw;
+  uint32_t highest = 0;  // entry, as unsigned: told at the end if it is no assignment
+  auto checked = [&](uint32_t raw) {
+    highest = max(highest, raw);
+    return min(raw, static_cast<uint32_t>(n) - 1);
   };
-  // Issue step kb. The next step's rows are looked up before its data, so that
-  // waiting for them does not wait for the data.
-  auto issue = [&](int kb) {
-    char* sr = smem + (kb % S) * STAGE + wave * 1024;
+  const char* dy = static_cast<const char*>(a.dy);
+  const char* x = static_cast<const char*>(a.x);
+  // Issue step kb into a stage. The next step's rows are looked up before its
+  // data, so that waiting for them does not wait for the data.
+  auto issue = [&](int kb, int st, auto whole_) {
+    char* sr = smem + st + wave * 1024;
     char* sc = sr + RB;
-    const char* dy = static_cast<const char*>(a.dy);
-    const char* x = static_cast<const char*>(a.x);
-    uint64_t rr[NR], cr[NC];
-    if (a.dy_order != kBucket) {
+    const char* rp[NR];
+    const char* cp[NC];
+    if constexpr (LOOKUP) {
+      // not before the barrier: the compiler would wait for the look-up there
 #pragma unroll
-      for (int i = 0; i < NR; ++i) rr[i] = static_cast<uint64_t>(row(rraw[i], a.dy_order)) * rld + rcol[i];
-    }
-    if (a.x_order != kBucket) {
+      for (int i = 0; i < NR; ++i) asm volatile("" : "+v"(rraw[i]));
 #pragma unroll
-      for (int i = 0; i < NC; ++i) cr[i] = static_cast<uint64_t>(row(craw[i], a.x_order)) * cld + ccol[i];
-    }
-    look_up(kb + 1);
-    const char* dy0 = dy + static_cast<int64_t>(lo + kb * BK) * rld;
-    const char* x0 = x + static_cast<int64_t>(lo + kb * BK) * cld;
-    if (kb < full) {
-      if (a.dy_order == kBucket) {
+      for (int i = 0; i < NC; ++i) asm volatile("" : "+v"(craw[i]));
 #pragma unroll
-        for (int i = 0; i < NR; ++i) load_lds16(dy0 + rcol[i], sr + i * NT * 16);
-      } else {
+      for (int i = 0; i < NR; ++i)
+        rp[i] = dy + rcol[i] + static_cast<uint64_t>(checked(a.dy_order == kBucket ? rpos(kb, i) : rraw[i])) * rld;
 #pragma unroll
-        for (int i = 0; i < NR; ++i) load_lds16(dy + rr[i], sr + i * NT * 16);
+      for (int i = 0; i < NC; ++i) {
+        const uint32_t r = checked(a.x_order == kBucket ? cpos(kb, i) : craw[i]);
+        cp[i] = x + ccol[i] + static_cast<uint64_t>(__umulhi(2 * r, a.k_magic) >> a.k_shift) * cld;
       }
-      if (a.x_order == kBucket) {
+      look_up(kb + 1);
+    } else {
+      const char* dy0 = dy + static_cast<int64_t>(lo + kb * BK) * rld;
+      const char* x0 = x + static_cast<int64_t>(lo + kb * BK) * cld;
 #pragma unroll
-        for (int i = 0; i < NC; ++i) load_lds16(x0 + ccol[i], sc + i * NT * 16);
-      } else {
+      for (int i = 0; i < NR; ++i) rp[i] = dy0 + rcol[i];
 #pragma unroll
-        for (int i = 0; i < NC; ++i) load_lds16(x + cr[i], sc + i * NT * 16);
-      }
+      for (int i = 0; i < NC; ++i) cp[i] = x0 + ccol[i];
+    }
+    if (decltype(whole_)::value || kb < full) {
+#pragma unroll
+      for (int i = 0; i < NR; ++i) load_lds16(rp[i], sr + i * NT * 16);
+#pragma unroll
+      for (int i = 0; i < NC; ++i) load_lds16(cp[i], sc + i * NT * 16);
     } else {  // zeros behind the bucket's end
       const u32x4_t zero = {0, 0, 0, 0};
 #pragma unroll
       for (int i = 0; i < NR; ++i) {
         if (kb * BK + rq + i * (NT / RPR) < count)
-          load_lds16(a.dy_order == kBucket ? dy0 + rcol[i] : dy + rr[i], sr + i * NT * 16);
+          load_lds16(rp[i], sr + i * NT * 16);
         else
           *reinterpret_cast<u32x4_t*>(sr + i * NT * 16 + lane * 16) = zero;
       }
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         if (kb * BK + cq + i * (NT / CPR) < count)
-          load_lds16(a.x_order == kBucket ? x0 + ccol[i] : x + cr[i], sc + i * NT * 16);
+          load_lds16(cp[i], sc + i * NT * 16);
         else
           *reinterpret_cast<u32x4_t*>(sc + i * NT * 16 + lane * 16) = zero;
       }
@@ -658,16 +655,16 @@ __global__ __launch_bounds__(256, 2) void k_tile_dw(DwArgs a, int64_t pairs, int
   // multiplied, across the barrier too.
   constexpr int G = TR / 4;
   u32x4_t cf[2][TC], rf[2][4];
-  auto cols = [&](int kb, u32x4_t(&f)[TC]) {
+  auto cols = [&](int st, u32x4_t(&f)[TC]) {
     int at4[4];
 #pragma unroll
-    for (int q = 0; q < TC; ++q) at4[q] = ca[q] + (kb % S) * STAGE;
+    for (int q = 0; q < TC; ++q) at4[q] = ca[q] + st;
     lds_tr_x4<0, 8 * BN>(at4, f);
   };
-  auto rows = [&](int kb, int grp, u32x4_t(&f)[4]) {
+  auto rows = [&](int st, int grp, u32x4_t(&f)[4]) {
     int at4[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) at4[q] = ra[grp * 4 + q] + (kb % S) * STAGE;
+    for (int q = 0; q < 4; ++q) at4[q] = ra[grp * 4 + q] + st;
     lds_tr_x4<0, 8 * BM>(at4, f);
   };
   auto products = [&](int grp, const u32x4_t(&c)[TC], const u32x4_t(&r)[4]) {
@@ -676,44 +673,62 @@ __global__ __launch_bounds__(256, 2) void k_tile_dw(DwArgs a, int64_t pairs, int
 #pragma unroll
       for (int q = 0; q < TC; ++q) acc[grp * 4 + v][q] = mma16<TYPE>(c[q], r[v], acc[grp * 4 + v][q]);
   };
-  // step kb has landed; step kb + 1, if it is whole, may be in flight
-  auto arrive = [&](int kb) {
-    if (kb + 1 < full)
-      barrier_keep<LOADS>();
-    else
-      barrier_keep<0>();
-    if (kb + 2 < steps) issue(kb + 2);
-  };
-  auto step = [&](int kb, auto odd_) {
+  // Step kb reads stage s0 and, across the barrier, the first fragments of the
+  // next step from s1; step kb + 3 is issued into s0 behind that barrier. The
+  // barrier leaves step kb + 2 in flight where it is whole. INNER: step kb + 3
+  // is whole too, so that nothing branches.
+  int s0 = 0, s1 = STAGE, s2 = 2 * STAGE;
+  auto step = [&](int kb, auto odd_, auto inner_) {
     constexpr int P = decltype(odd_)::value;  // kb % 2
+    constexpr bool INNER = decltype(inner_)::value;
     if constexpr (G == 2) {
-      rows(kb, 1, rf[1]);
+      rows(s0, 1, rf[1]);
       products(0, cf[P], rf[0]);
     }
-    if (kb + 1 < steps) {
-      arrive(kb + 1);
-      cols(kb + 1, cf[P ^ 1]);
-      rows(kb + 1, 0, rf[G == 2 ? 0 : P ^ 1]);
+    if (INNER || kb + 1 < steps) {
+      if (INNER || kb + 2 < full)
+        barrier_keep<LOADS>();
+      else
+        barrier_keep<0>();
+      if (INNER || kb + 3 < steps) issue(kb + 3, s0, inner_);
+      cols(s1, cf[P ^ 1]);
+      rows(s1, 0, rf[G == 2 ? 0 : P ^ 1]);
     }
     if constexpr (G == 2)
       products(1, cf[P], rf[1]);
     else
       products(0, cf[P], rf[P]);
+    const int t = s0;
+    s0 = s1;
+    s1 = s2;
+    s2 = t;
   };
 
-  look_up(0);
-  if (steps > 0) issue(0);
-  if (steps > 1) issue(1);
+  const std::integral_constant<int, 0> even;
+  const std::integral_constant<int, 1> odd;
   if (steps > 0) {
-    arrive(0);
+    look_up(0);
+    issue(0, 0, std::false_type{});
+    if (steps > 1) issue(1, STAGE, std::false_type{});
+    if (1 < full)
+      barrier_keep<LOADS>();
+    else
+      barrier_keep<0>();
+    if (steps > 2) issue(2, 2 * STAGE, std::false_type{});
     cols(0, cf[0]);
     rows(0, 0, rf[0]);
   }
-  for (int kb = 0; kb < steps; kb += 2) {
-    step(kb, std::integral_constant<int, 0>{});
-    if (kb + 1 < steps) step(kb + 1, std::integral_constant<int, 1>{});
+  int kb = 0;
+  for (; kb + 4 < full; kb += 2) {
+    step(kb, even, std::true_type{});
+    step(kb + 1, odd, std::true_type{});
+  }
+  for (; kb < steps; kb += 2) {
+    step(kb, even, std::false_type{});
+    if (kb + 1 < steps) step(kb + 1, odd, std::false_type{});
   }
 
+  if (highest >= static_cast<uint32_t>(n) && count > 0) set_device_error(a.err, 16);
   const int osize = a.out_type == 1 ? 4 : 2;
 #pragma unroll
   for (int i = 0; i < TR; ++i) {
@@ -802,12 +817,26 @@ hipError_t launch_dw(const DwArgs& a, hipStream_t s) {
   const int run = static_cast<int>(std::min<int64_t>(32, (pairs + 7) / 8));
   const int64_t grid = (pairs + 8 * run - 1) / (8 * run) * (8 * run);
   if (grid > INT32_MAX) return hipErrorInvalidValue;
-  QSMOE_LAUNCH((k_tile_dw<TYPE, BM, BN>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, a, pairs, run);
+  if (a.x_order == kBucket && a.dy_order == kBucket)
+    QSMOE_LAUNCH((k_tile_dw<TYPE, BM, BN, false>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, a, pairs, run);
+  else
+    QSMOE_LAUNCH((k_tile_dw<TYPE, BM, BN, true>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, a, pairs, run);
   return hipGetLastError();
 }
 
+// r / d for every r < 2^31 as umulhi(2 r, magic) >> shift: with shift =
+// ceil(log2 d) and magic = ceil(2^(31 + shift) / d), the product exceeds
+// r * 2^(31 + shift) / d by less than 2^31 <= 2^(31 + shift) / d.
+void set_divisor(DwArgs& a) {
+  const uint32_t d = a.x_order == kToken ? a.k : 1;
+  a.k_shift = 0;
+  while ((uint64_t{1} << a.k_shift) < d) ++a.k_shift;
+  a.k_magic = static_cast<uint32_t>(((uint64_t{1} << (31 + a.k_shift)) + d - 1) / d);
+}
+
 template <int TYPE>
-hipError_t pick_dw(const DwArgs& a, hipStream_t s) {
+hipError_t pick_dw(DwArgs a, hipStream_t s) {
+  set_divisor(a);
   const int64_t pairs = static_cast<int64_t>(a.E) * ((a.N + 255) / 256) * ((a.K + 127) / 128);
   if (pairs >= 512) return launch_dw<TYPE, 256, 128>(a, s);
   return launch_dw<TYPE, 128, 128>(a, s);
