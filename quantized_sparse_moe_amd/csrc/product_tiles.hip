@@ -706,22 +706,27 @@ __global__ __launch_bounds__(256, 2) void k_tile_dw(DwArgs a, int64_t pairs, int
 
   const std::integral_constant<int, 0> even;
   const std::integral_constant<int, 1> odd;
-  if (steps > 0) {
+  auto begin = [&](auto whole) {
     look_up(0);
-    issue(0, 0, std::false_type{});
-    if (steps > 1) issue(1, STAGE, std::false_type{});
-    if (1 < full)
+    issue(0, 0, whole);
+    if (decltype(whole)::value || steps > 1) issue(1, STAGE, whole);
+    if (decltype(whole)::value || 1 < full)
       barrier_keep<LOADS>();
     else
       barrier_keep<0>();
-    if (steps > 2) issue(2, 2 * STAGE, std::false_type{});
+    if (decltype(whole)::value || steps > 2) issue(2, 2 * STAGE, whole);
     cols(0, cf[0]);
     rows(0, 0, rf[0]);
-  }
+  };
   int kb = 0;
-  for (; kb + 4 < full; kb += 2) {
-    step(kb, even, std::true_type{});
-    step(kb + 1, odd, std::true_type{});
+  if (full > 4) {  // a beginning of its own, or the loop waits as if steps before it might be partial
+    begin(std::true_type{});
+    for (; kb + 4 < full; kb += 2) {
+      step(kb, even, std::true_type{});
+      step(kb + 1, odd, std::true_type{});
+    }
+  } else if (steps > 0) {
+    begin(std::false_type{});
   }
   for (; kb < steps; kb += 2) {
     step(kb, even, std::false_type{});
