@@ -122,7 +122,7 @@ __global__ __launch_bounds__(256) void k_quantize_rows(const typename Elem<DT>::
       load16<DT>(p, v);
       load16<DT>(p + cols, u);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = silu(v[i]) * u[i];
+      for (int i = 0; i < 16; ++i) v[i] = silu_fast(v[i]) * u[i];
     } else {
       load16<DT>(src + row * cols + c, v);
     }
