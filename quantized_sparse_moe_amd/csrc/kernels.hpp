@@ -145,6 +145,9 @@ hipError_t launch_quantize_block(const void* x, int dtype, int64_t matrices, int
 hipError_t launch_swiglu_quantize_block(const void* gu, int dtype, int64_t rows, int inner, int pow2, uint8_t* codes,
                                         float* scales, int32_t* err, hipStream_t s);
 
+// HIP counts a grid's threads with 32 bits.
+constexpr int64_t max_workgroups(int threads) { return (int64_t{1} << 32) / threads - 1; }
+
 // Products grouped by expert ----------------------------------------------------
 constexpr int kTypeE4m3 = 3;  // element type beside moe_dtype's, with scales
 

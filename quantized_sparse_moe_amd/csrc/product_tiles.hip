@@ -756,7 +756,7 @@ hipError_t launch_tiles(const ProductArgs& a, hipStream_t s) {
   const int64_t pairs = (a.offsets ? n / BM + std::min<int64_t>(a.E, n) : (n + BM - 1) / BM) * ctiles;
   const int run = static_cast<int>(std::min<int64_t>(32, (pairs + 7) / 8));
   const int64_t grid = (pairs + 8 * run - 1) / (8 * run) * (8 * run);
-  if (grid > INT32_MAX) return hipErrorInvalidValue;
+  if (grid > max_workgroups(WM * WN * 64)) return hipErrorInvalidValue;
   QSMOE_LAUNCH((k_tile_product<TYPE, BM, BN, WM, WN, S, CT>), dim3(static_cast<unsigned>(grid)), dim3(WM * WN * 64), 0,
                s, a, run);
   return hipGetLastError();
@@ -769,7 +769,7 @@ hipError_t launch_split(const ProductArgs& a, hipStream_t s) {
       (a.offsets ? n / (16 * RT) + std::min<int64_t>(a.E, n) : (n + 16 * RT - 1) / (16 * RT)) * ((a.C + 15) / 16);
   const int run = static_cast<int>(std::min<int64_t>(32, (pairs + 7) / 8));
   const int64_t grid = (pairs + 8 * run - 1) / (8 * run) * (8 * run);
-  if (grid > INT32_MAX) return hipErrorInvalidValue;
+  if (grid > max_workgroups(256)) return hipErrorInvalidValue;
   QSMOE_LAUNCH((k_split_product<TYPE, RT>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, a, run);
   return hipGetLastError();
 }
@@ -821,7 +821,7 @@ hipError_t launch_dw(const DwArgs& a, hipStream_t s) {
   // with runs of 64, 646 with 32, 670 with 16).
   const int run = static_cast<int>(std::min<int64_t>(32, (pairs + 7) / 8));
   const int64_t grid = (pairs + 8 * run - 1) / (8 * run) * (8 * run);
-  if (grid > INT32_MAX) return hipErrorInvalidValue;
+  if (grid > max_workgroups(256)) return hipErrorInvalidValue;
   if (a.x_order == kBucket && a.dy_order == kBucket)
     QSMOE_LAUNCH((k_tile_dw<TYPE, BM, BN, false>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, a, pairs, run);
   else

@@ -179,7 +179,7 @@ template <int DT, bool SWIGLU>
 hipError_t launch_rows(const void* x, int64_t rows, int cols, int pow2, uint8_t* codes, float* scales, int32_t* err,
                        hipStream_t s) {
   const int64_t groups = (rows * ((cols + 127) / 128) + 31) / 32;
-  if (groups > INT32_MAX) return hipErrorInvalidValue;
+  if (groups > max_workgroups(256)) return hipErrorInvalidValue;
   QSMOE_LAUNCH((k_quantize_rows<DT, SWIGLU>), dim3(static_cast<unsigned>(groups)), dim3(256), 0, s,
                static_cast<const typename Elem<DT>::type*>(x), rows, cols, pow2, codes, scales, err);
   return hipGetLastError();
@@ -189,7 +189,8 @@ template <int DT>
 hipError_t launch_tiles(const void* x, int64_t matrices, int64_t rows, int cols, int pow2, uint8_t* codes,
                         float* scales, int32_t* err, hipStream_t s) {
   const int64_t rb = (rows + 127) / 128, nb = (cols + 127) / 128;
-  if (matrices > INT32_MAX / rb || matrices * rb > INT32_MAX / nb) return hipErrorInvalidValue;
+  constexpr int64_t most = max_workgroups(256);
+  if (matrices > most / rb || matrices * rb > most / nb) return hipErrorInvalidValue;
   QSMOE_LAUNCH((k_quantize_tiles<DT>), dim3(static_cast<unsigned>(matrices * rb * nb)), dim3(256), 0, s,
                static_cast<const typename Elem<DT>::type*>(x), rows, cols, rb, pow2, codes, scales, err);
   return hipGetLastError();

@@ -158,6 +158,77 @@ def test_matmul_block(M, N, K, out):
     close(y, a64 @ b64.T, np.abs(a64) @ np.abs(b64).T, K, out, fp8=True)
 
 
+# Sizes that reach each tile size and the steps in the middle of a long contraction: rows x columns that fill the chip
+# with 256 x 256 tiles, with 128 x 256 (ragged and dense), with 128 x 128 and 64 x 128 ones. Columns, contraction, rows.
+FILL = [(4100, 1, 4, 4104, 528, "skew"), (2050, 3, 64, 2056, 656, "even"), (1000, 2, 16, 2056, 1296, "skew"),
+        (900, 4, 128, 1032, 400, "skew")]
+
+
+@pytest.mark.parametrize("T,k,E,C,Q,kind", FILL)
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_grouped_matmul_that_fills_the_chip(T, k, E, C, Q, kind, transposed, dtype):
+    rng = np.random.default_rng(case_seed(T, E, C, int(transposed), dtype))
+    off, perm = buckets(T, T, k, E, kind)
+    x, w = ints(rng, T, Q), ints(rng, E, *((Q, C) if transposed else (C, Q)))
+    y = qm.grouped_matmul(dev(x, DT[dtype]), dev(w, DT[dtype]), dev(off), perm=dev(perm), top_k=k, x_order="token",
+                          out_order="slot", transposed=transposed, out_dtype="f32")
+    # |sums| <= 16 * 1296 < 2^24: exact in float32 on the host too
+    want = np.empty((T * k, C), np.float32)
+    for e in range(E):
+        p = perm[off[e]:off[e + 1]]
+        want[p] = x[p // k] @ (w[e] if transposed else w[e].T)
+    assert np.array_equal(y.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("T,k,E,N,K,kind", FILL)
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_grouped_matmul_block_that_fills_the_chip(T, k, E, N, K, kind, out):
+    """Codes and scales that make every product and sum exact, with 13 bits below the largest product too: integers up
+    to 4, and scales that are powers of two."""
+    rng = np.random.default_rng(case_seed(T, E, N, out))
+    off, perm = buckets(T, T, k, E, kind)
+    nb = -(-K // 128)
+    av, wv = ints(rng, T, K), ints(rng, E, N, K)
+    sa = np.exp2(rng.integers(-1, 2, (T, nb))).astype(np.float32)
+    sw = np.exp2(rng.integers(-1, 2, (E, -(-N // 128), nb))).astype(np.float32)
+    y = qm.grouped_matmul_block(dev(oracle.e4m3_encode(av)), dev(sa), dev(oracle.e4m3_encode(wv)), dev(sw), dev(off),
+                                perm=dev(perm), top_k=k, x_order="token", out_dtype=out)
+    a32 = av * np.repeat(sa, 128, 1)[:, :K]
+    want = np.empty((T * k, N), np.float32)
+    for e in range(E):
+        w32 = wv[e] * np.repeat(np.repeat(sw[e], 128, 0)[:N], 128, 1)[:, :K]
+        want[off[e]:off[e + 1]] = a32[perm[off[e]:off[e + 1]] // k] @ w32.T
+    want = torch.from_numpy(want).to(DT[out])
+    assert torch.equal(y.cpu(), want)
+
+
+@pytest.mark.parametrize("M,N,K", [(4096, 4104, 528), (2100, 4096, 656), (1100, 4104, 400), (500, 4096, 1296)])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_matmul_block_that_fills_the_chip(M, N, K, out):
+    rng = np.random.default_rng(case_seed(M, N, K, out))
+    nb = -(-K // 128)
+    av, bv = ints(rng, M, K), ints(rng, N, K)
+    sa = np.exp2(rng.integers(-1, 2, (M, nb))).astype(np.float32)
+    sb = np.exp2(rng.integers(-1, 2, (-(-N // 128), nb))).astype(np.float32)
+    y = qm.matmul_block(dev(oracle.e4m3_encode(av)), dev(sa), dev(oracle.e4m3_encode(bv)), dev(sb), out_dtype=out)
+    want = (av * np.repeat(sa, 128, 1)[:, :K]) @ (bv * np.repeat(np.repeat(sb, 128, 0)[:N], 128, 1)[:, :K]).T
+    assert torch.equal(y.cpu(), torch.from_numpy(want).to(DT[out]))
+
+
+@pytest.mark.parametrize("T,k,E,N,K,kind", [(2000, 2, 16, 1032, 1032, "skew"), (1500, 1, 3, 520, 264, "even")])
+@pytest.mark.parametrize("orders", [("bucket", "bucket"), ("token", "slot"), ("slot", "bucket")], ids="-".join)
+def test_weight_gradient_of_long_buckets(T, k, E, N, K, kind, orders):
+    rng = np.random.default_rng(case_seed(T, E, N, *orders))
+    off, perm = buckets(T, T, k, E, kind)
+    x, dy = ints(rng, T if orders[0] == "token" else T * k, K), ints(rng, T * k, N)
+    dw = qm.grouped_matmul_dw(dev(x, DT["bf16"]), dev(dy, DT["bf16"]), dev(off), perm=dev(perm), top_k=k,
+                              x_order=orders[0], dy_order=orders[1])
+    xs, ds = oracle.source_rows(x, orders[0], perm, k), oracle.source_rows(dy, orders[1], perm, k)
+    want = np.stack([ds[off[e]:off[e + 1]].T @ xs[off[e]:off[e + 1]] for e in range(E)])
+    assert np.array_equal(dw.cpu().numpy(), want)
+
+
 # ------------------------------------------------------------------ exact on integers
 
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
