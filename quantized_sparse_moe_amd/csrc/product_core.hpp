@@ -154,6 +154,31 @@ __device__ __forceinline__ void store8(char* p, int out_type, f32x4_t v, f32x4_t
   }
 }
 
+// fp32 results of two neighbouring 16 x 16 fragments, whole 128-byte lines at
+// a time: lane (g, j) holds columns 4 g .. + 3 of both in row j; lanes j and
+// j ^ 8 trade, so that the first store writes 32 columns of rows 0 .. 7 and
+// the second those of rows 8 .. 15. row_ptr(r): address of the first
+// fragment's first column in row r, or null; left: columns that exist.
+template <typename F>
+__device__ __forceinline__ void store_pair_f32(f32x4_t f0, f32x4_t f1, int left, F row_ptr) {
+  const int lane = lane_id(), g = lane >> 4, j = lane & 15;
+  const bool low = j < 8;
+  f32x4_t first, second;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const float traded = __int_as_float(
+        __builtin_amdgcn_update_dpp(0, __float_as_int(low ? f1[v] : f0[v]), 0x128, 0xf, 0xf, true));  // row_ror:8
+    first[v] = low ? f0[v] : traded;
+    second[v] = low ? traded : f1[v];
+  }
+  const int c = (low ? 0 : 16) + 4 * g;
+  if (c >= left) return;
+  float* p = row_ptr(j & 7);
+  if (p) *reinterpret_cast<f32x4_t*>(p + c) = first;
+  p = row_ptr(8 + (j & 7));
+  if (p) *reinterpret_cast<f32x4_t*>(p + c) = second;
+}
+
 // Inclusive sum over the wave's lanes: rows of 16 by DPP shifts, then the row
 // totals handed on.
 __device__ __forceinline__ int wave_scan(int v) {

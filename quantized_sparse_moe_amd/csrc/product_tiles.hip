@@ -734,16 +734,29 @@ __global__ __launch_bounds__(256, 2) void k_tile_dw(DwArgs a, int64_t pairs, int
   }
 
   if (highest >= static_cast<uint32_t>(n) && count > 0) set_device_error(a.err, 16);
-  const int osize = a.out_type == 1 ? 4 : 2;
+  if (a.out_type == 1) {
+#pragma unroll
+    for (int i = 0; i < TR; ++i) {
+#pragma unroll
+      for (int q = 0; q < TC; q += 2) {
+        const int c = c0 + (wn * TC + q) * 16;
+        store_pair_f32(acc[i][q], acc[i][q + 1], a.K - c, [&](int r) -> float* {
+          const int row = r0 + (wm * TR + i) * 16 + r;
+          return row < a.N ? static_cast<float*>(a.out) + (static_cast<int64_t>(e) * a.N + row) * a.K + c : nullptr;
+        });
+      }
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < TR; ++i) {
     const int r = r0 + (wm * TR + i) * 16 + j;
     if (r >= a.N) continue;
-    char* o = static_cast<char*>(a.out) + (static_cast<int64_t>(e) * a.N + r) * a.K * osize;
+    char* o = static_cast<char*>(a.out) + (static_cast<int64_t>(e) * a.N + r) * a.K * 2;
 #pragma unroll
     for (int q = 0; q < TC; ++q) {
       const int c = c0 + (wn * TC + q) * 16 + 4 * g;
-      if (c < a.K) store4(o + static_cast<int64_t>(c) * osize, a.out_type, acc[i][q]);
+      if (c < a.K) store4(o + static_cast<int64_t>(c) * 2, a.out_type, acc[i][q]);
     }
   }
 }
