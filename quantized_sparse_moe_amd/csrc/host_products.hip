@@ -19,13 +19,14 @@ moe_status hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_
 
 bool is_dtype(int32_t d) { return d == MOE_DT_BF16 || d == MOE_DT_F32 || d == MOE_DT_F16; }
 
-// The kernels index one expert's matrix and its tiles with 32 bits.
-constexpr int32_t kMaxSide = 1 << 20;
+// The kernels index one expert's tiles and all positions, rounded up to a
+// tile, with 32 bits.
+constexpr int32_t kMaxSide = 1 << 20, kMaxRows = 1 << 30;
 
 moe_status check_groups(int32_t T, int32_t k, int32_t N, int32_t K, int32_t E) {
   if (T < 0 || k < 1 || N < 0 || K < 0 || E < 1) return MOE_ERR_INVALID_ARG;
   if (static_cast<int64_t>(T) * k > INT32_MAX) return MOE_ERR_INVALID_ARG;
-  if (E > 1024 || N > kMaxSide || K > kMaxSide) return MOE_ERR_UNSUPPORTED;
+  if (E > 1024 || N > kMaxSide || K > kMaxSide || T * k > kMaxRows) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

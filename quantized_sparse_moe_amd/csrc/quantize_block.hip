@@ -8,7 +8,11 @@
 //
 // Both kernels read each element once and hold it in registers between the
 // maximum and the conversion, 16 elements per lane, so that a lane's codes
-// leave as one 16-byte store; memory bounds them.
+// leave as one 16-byte store; memory bounds them. 32 x [2048][4096] bf16
+// weights in 128 x 128 blocks: 149 us, 5.4 TB/s (a large copy: 4.9). The
+// SwiGLU's sigmoid takes a reciprocal (at most 3 ulp from the division):
+// 24576 rows of 2048 43 us, 5.9 TB/s; with the division the VALU bounds it at
+// 55 us. One row of 4096: 7.2 us a call, the host's side of it.
 #include "common.hpp"
 #include "kernels.hpp"
 

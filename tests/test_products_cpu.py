@@ -54,6 +54,7 @@ def dense(a=F, sa=F, b=F, sb=F, M=2, N=8, K=16, out_dtype=0, out=F):
 @pytest.mark.parametrize("kw,status", [
     (dict(M=-1), INVALID), (dict(N=-8), INVALID), (dict(K=-16), INVALID), (dict(out_dtype=3), INVALID),
     (dict(K=24), UNSUPPORTED), (dict(N=12), UNSUPPORTED), (dict(N=(1 << 20) + 8), UNSUPPORTED),
+    (dict(M=(1 << 30) + 1), UNSUPPORTED),
     (dict(K=(1 << 20) + 16), UNSUPPORTED), (dict(a=None), INVALID), (dict(sa=None), INVALID), (dict(b=None), INVALID),
     (dict(sb=None), INVALID), (dict(out=None), INVALID), (dict(a=F + 8), ALIGNMENT), (dict(b=F + 1), ALIGNMENT),
     (dict(sa=F + 2), ALIGNMENT), (dict(sb=F + 2), ALIGNMENT), (dict(out=F + 8), ALIGNMENT),
@@ -83,7 +84,7 @@ def grouped_dw(x=F, dy=F, dtype=0, T=2, k=2, N=8, K=8, E=4, offsets=F, perm=F, x
 
 SHARED = [
     (dict(T=-1), INVALID), (dict(k=0), INVALID), (dict(N=-8), INVALID), (dict(K=-16), INVALID), (dict(E=0), INVALID),
-    (dict(T=1 << 30, k=2), INVALID), (dict(E=1025), UNSUPPORTED), (dict(N=(1 << 20) + 16), UNSUPPORTED),
+    (dict(T=1 << 30, k=2), INVALID), (dict(T=(1 << 30) + 1, k=1), UNSUPPORTED), (dict(E=1025), UNSUPPORTED), (dict(N=(1 << 20) + 16), UNSUPPORTED),
     (dict(K=(1 << 20) + 16), UNSUPPORTED), (dict(N=12), UNSUPPORTED), (dict(out_dtype=5), INVALID),
     (dict(offsets=None), INVALID), (dict(out=None), INVALID), (dict(offsets=F + 2), ALIGNMENT),
     (dict(perm=F + 2), ALIGNMENT), (dict(out=F + 8), ALIGNMENT), (dict(err=F + 2), ALIGNMENT),
