@@ -817,7 +817,7 @@ hipError_t pick_tiles(const ProductArgs& a, hipStream_t s) {
   // taken as half full (a bucket of fewer rows than h still takes one).
   const int64_t used = std::min<int64_t>(a.E, n);
   auto tiles = [&](int h, int w) {
-    const int64_t m = a.offsets ? std::max<int64_t>(used, n / h + used / 2) : (n + h - 1) / h;
+    const int64_t m = a.offsets ? std::max<int64_t>(used, n / h + (used + 1) / 2) : (n + h - 1) / h;
     return m * ((a.C + w - 1) / w);
   };
   // What a tile size gives was measured on dense FP8 products of 4096 x 4096
@@ -830,13 +830,22 @@ hipError_t pick_tiles(const ProductArgs& a, hipStream_t s) {
   // ragged buckets spread better (fp16, 24 buckets of 84 rows: 39 against
   // 55 us).
   if constexpr (!CT) {
-    // 16 columns of split contraction: 64 rows of 4096 x 4096 16 us against
-    // 19, 128 rows 28 against 19; one row 7.4 against 17
-    if (tiles(64, 128) <= 256) {
-      if (mean <= 16) return launch_split<TYPE, 1>(a, s);
-      if (mean <= 32) return launch_split<TYPE, 2>(a, s);
-      if (mean <= 64 && tiles(64, 128) <= 32) return launch_split<TYPE, 4>(a, s);
-    }
+    // 16 columns of split contraction. A round of 256 of its workgroups takes
+    // 7 / 10 / 15 us for 16 / 32 / 64 rows (FP8, contraction 4096) where one of
+    // 64 x 128 tiles takes 18 however few there are: 305 rows by 240 columns 9
+    // us against 17, 16 by 8192 12 against 17; where none of the conditions
+    // holds it loses, 64 rows by 6144 columns 38 against 19.
+    auto parts = [&](int rt) { return tiles(16 * rt, 16); };
+    // Buckets of a few rows read each weight once either way, and more waves
+    // read them faster (bf16, 8 experts of 2048 x 2048: 4 rows each 14 us
+    // against 19, 15 rows 21 against 19; 16 of 512 x 2048: 15 rows 14 against
+    // 20).
+    if (mean <= 8 && tiles(64, 128) <= 256) return launch_split<TYPE, 1>(a, s);
+    if (mean <= 16 && tiles(64, 128) <= 96) return launch_split<TYPE, 1>(a, s);
+    if (parts(1) <= 256) return launch_split<TYPE, 1>(a, s);
+    if (parts(2) <= 384) return launch_split<TYPE, 2>(a, s);
+    if (parts(1) <= 512) return launch_split<TYPE, 1>(a, s);
+    if (parts(4) <= 256) return launch_split<TYPE, 4>(a, s);
   }
   if constexpr (TYPE != kE4m3Wide) {
     if (mean >= 192 && tiles(256, 256) >= 192) return launch_tiles<TYPE, 256, 256, 2, 4, 2, CT>(a, s);

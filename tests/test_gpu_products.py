@@ -216,6 +216,34 @@ def test_matmul_block_that_fills_the_chip(M, N, K, out):
     assert torch.equal(y.cpu(), torch.from_numpy(want).to(DT[out]))
 
 
+# Few tiles and a contraction that is shared out: one, two and four row tiles of 16 at a time. Rows, experts, columns,
+# contraction.
+@pytest.mark.parametrize("T,E,C,Q", [(40, 2, 520, 1296), (200, 2, 520, 1040), (200, 2, 1000, 1040), (305, 1, 240, 1296),
+                                     (200, 1, 1000, 656), (90, 5, 264, 2000)])
+@pytest.mark.parametrize("out", ["f32", "bf16", "f16"])
+def test_few_tiles_share_the_contraction(T, E, C, Q, out):
+    rng = np.random.default_rng(case_seed(T, E, C, out))
+    off, perm = buckets(T, T, 1, E, "skew")
+    nb = -(-Q // 128)
+    av, wv = ints(rng, T, Q), ints(rng, E, C, Q)
+    want = np.empty((T, C), np.float32)
+    for e in range(E):
+        p = perm[off[e]:off[e + 1]]
+        want[p] = av[p] @ wv[e].T
+    kw = dict(perm=dev(perm), top_k=1, x_order="token", out_order="slot", out_dtype=out)
+    if out != "f32":
+        y = qm.grouped_matmul(dev(av, DT[out]), dev(wv, DT[out]), dev(off), **kw)
+        assert torch.equal(y.cpu(), torch.from_numpy(want).to(DT[out]))
+    codes, scales = oracle.e4m3_encode(wv), np.ones((E, -(-C // 128), nb), np.float32)
+    y = qm.grouped_matmul_block(dev(oracle.e4m3_encode(av)), dev(np.ones((T, nb), np.float32)), dev(codes),
+                                dev(scales), dev(off), **kw)
+    assert torch.equal(y.cpu(), torch.from_numpy(want).to(DT[out]))
+    if E == 1:
+        y = qm.matmul_block(dev(oracle.e4m3_encode(av)), dev(np.ones((T, nb), np.float32)), dev(codes[0]),
+                            dev(scales[0]), out_dtype=out)
+        assert torch.equal(y.cpu(), torch.from_numpy(want).to(DT[out]))
+
+
 @pytest.mark.parametrize("T,k,E,N,K,kind", [(2000, 2, 16, 1032, 1032, "skew"), (1500, 1, 3, 520, 264, "even")])
 @pytest.mark.parametrize("orders", [("bucket", "bucket"), ("token", "slot"), ("slot", "bucket")], ids="-".join)
 def test_weight_gradient_of_long_buckets(T, k, E, N, K, kind, orders):
