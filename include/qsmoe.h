@@ -427,7 +427,8 @@ moe_status moe_swiglu_quantize_block(const void* gu, int32_t dtype, int64_t rows
  * matrix instruction forms a block's sum: it adds 8 neighbouring products with
  * 13 bits below the largest of them (an error of 2e-5 of the result in the
  * norm, rounding to fp16 being 2.1e-4; at most 7 * 2^-13 of a group's largest
- * product), the groups in fp32.
+ * product), the groups in fp32. The two scales are multiplied with each other
+ * first, in fp32: a pair whose product leaves its normal range loses accuracy.
  *   a [M][K] codes, a_scales [M][ceil(K / 128)]              (1 x 128)
  *   b [N][K] codes, b_scales [ceil(N / 128)][ceil(K / 128)]  (128 x 128)
  *   out [M][N], out_dtype MOE_DT_BF16, MOE_DT_F32 or MOE_DT_F16

@@ -374,6 +374,12 @@ def _shape(t: torch.Tensor, name: str, shape) -> None:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _sides(*sizes: int) -> None:
+    """ctypes would pass on the low 32 bits of a size that the ABI takes in 32."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise ValueError(f"sizes must be below 2^31, got {sizes}")
+
+
 def _elsewhere(device: torch.device, stream) -> bool:
     """Whether a call has to make another device or stream current first."""
     return stream is not None or device.index != torch.cuda.current_device()
@@ -383,6 +389,8 @@ def _elsewhere(device: torch.device, stream) -> bool:
 def _on(device: torch.device, stream):
     """`device` current and, if a stream is given, that stream too, so that what
     a call allocates belongs to the stream its kernels run on."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the operands on {device}")
     with torch.cuda.device(device), torch.cuda.stream(stream):
         yield
 
@@ -418,6 +426,7 @@ def quantize_block(x: torch.Tensor, block_rows: int = 1, pow2: bool = False, err
         with _on(dev, stream):
             return quantize_block(x, block_rows, pow2, err)
     *lead, rows, cols = x.shape
+    _sides(cols, block_rows)
     codes = torch.empty_like(x, dtype=_E4M3)
     scales = torch.empty((*lead, -(-rows // max(block_rows, 1)), _blocks(cols)), dtype=torch.float32, device=dev)
     check(_lib.load().moe_quantize_block(x.data_ptr(), _DT[x.dtype], lead[0] if lead else 1, rows, cols, block_rows,
@@ -437,6 +446,7 @@ def swiglu_quantize_block(gu: torch.Tensor, pow2: bool = False, err: Optional[to
     if two % 2:
         raise ValueError("gu must hold gate and up columns in equal number")
     inner = two // 2
+    _sides(inner)
     codes = torch.empty((rows, inner), dtype=_E4M3, device=dev)
     scales = torch.empty((rows, _blocks(inner)), dtype=torch.float32, device=dev)
     check(_lib.load().moe_swiglu_quantize_block(gu.data_ptr(), _DT[gu.dtype], rows, inner, 1 if pow2 else 0,
@@ -454,6 +464,7 @@ def matmul_block(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_sca
     M, K = a.shape
     N = _operand(b, "b", _FP8, (2,), dev).shape[0]
     _shape(b, "b", (N, K))
+    _sides(M, N, K)
     _shape(_operand(a_scales, "a_scales", _F32, (2,), dev), "a_scales", (M, _blocks(K)))
     _shape(_operand(b_scales, "b_scales", _F32, (2,), dev), "b_scales", (_blocks(N), _blocks(K)))
     if _elsewhere(dev, stream):
@@ -465,8 +476,9 @@ def matmul_block(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_sca
     return y
 
 
-def _groups(rows: int, order: str, top_k: int, offsets: torch.Tensor, perm: Optional[torch.Tensor], E: int, dev):
-    """Checks of offsets and perm, and the token count of a matrix of `rows` rows in `order`."""
+def _groups(rows: int, order: str, top_k: int, offsets: torch.Tensor, perm: Optional[torch.Tensor], E: int, N: int,
+            K: int, dev):
+    """Checks of sizes, offsets and perm, and the token count of a matrix of `rows` rows in `order`."""
     if order not in _lib.MOE_ROWS:
         raise ValueError(f"row order must be one of {', '.join(_lib.MOE_ROWS)}, got {order!r}")
     if top_k < 1:
@@ -474,6 +486,7 @@ def _groups(rows: int, order: str, top_k: int, offsets: torch.Tensor, perm: Opti
     if order != "token" and rows % top_k:
         raise ValueError(f"{rows} rows in {order} order are no multiple of top_k = {top_k}")
     T = rows if order == "token" else rows // top_k
+    _sides(T * top_k, E, N, K)
     _shape(_operand(offsets, "offsets", _I32, (1,), dev), "offsets", (E + 1,))
     if perm is not None:
         _shape(_operand(perm, "perm", _I32, (1,), dev), "perm", (T * top_k,))
@@ -496,7 +509,7 @@ def grouped_matmul_block(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tenso
     _shape(a, "a", (rows, K))
     _shape(_operand(a_scales, "a_scales", _F32, (2,), dev), "a_scales", (rows, _blocks(K)))
     _shape(_operand(w_scales, "w_scales", _F32, (3,), dev), "w_scales", (E, _blocks(N), _blocks(K)))
-    T = _groups(rows, x_order, top_k, offsets, perm, E, dev)
+    T = _groups(rows, x_order, top_k, offsets, perm, E, N, K, dev)
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return grouped_matmul_block(a, a_scales, w, w_scales, offsets, perm, top_k, x_order, out_order, out_dtype,
@@ -522,7 +535,7 @@ def grouped_matmul(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, perm
     E, N, K = _operand(w, "w", (x.dtype,), (3,), dev).shape
     rows = x.shape[0]
     _shape(x, "x", (rows, N if transposed else K))
-    T = _groups(rows, x_order, top_k, offsets, perm, E, dev)
+    T = _groups(rows, x_order, top_k, offsets, perm, E, N, K, dev)
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return grouped_matmul(x, w, offsets, perm, top_k, x_order, out_order, transposed, out_dtype, out, err)
@@ -545,8 +558,8 @@ def grouped_matmul_dw(x: torch.Tensor, dy: torch.Tensor, offsets: torch.Tensor, 
     dev = _operand(x, "x", _B16, (2,)).device
     rows, K = x.shape
     N = _operand(dy, "dy", (x.dtype,), (2,), dev).shape[1]
-    E = offsets.shape[0] - 1 if offsets.dim() == 1 else 0
-    T = _groups(rows, x_order, top_k, offsets, perm, E, dev)
+    E = max(offsets.shape[0] - 1, 0) if offsets.dim() == 1 else 0
+    T = _groups(rows, x_order, top_k, offsets, perm, E, N, K, dev)
     _shape(dy, "dy", (T * top_k, N))
     if _elsewhere(dev, stream):
         with _on(dev, stream):

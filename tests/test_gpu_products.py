@@ -471,6 +471,34 @@ def test_refusals_on_the_device():
                         z(1, 1, d=torch.float32))
 
 
+def test_sizes_that_32_bits_do_not_hold_are_refused():
+    """2^32 rows would reach the ABI as none."""
+    z = lambda *s, d=torch.bfloat16: torch.zeros(*s, dtype=d, device="cuda")  # noqa: E731
+    off, rows = z(4, d=torch.int32), 1 << 32
+    with pytest.raises(ValueError):
+        qm.grouped_matmul(z(rows, 0), z(3, 8, 0), off)
+    with pytest.raises(ValueError):
+        qm.grouped_matmul(z(2, 16), z(3, 8, 16), off, x_order="token", top_k=1 << 31)
+    with pytest.raises(ValueError):
+        qm.grouped_matmul(z(0, 0), z(3, rows, 0), off)
+    with pytest.raises(ValueError):
+        qm.grouped_matmul_dw(z(4, 0), z(4, 16), off[:0])
+    with pytest.raises(ValueError):
+        qm.matmul_block(z(rows, 0, d=torch.uint8), z(rows, 0, d=torch.float32), z(8, 0, d=torch.uint8),
+                        z(1, 0, d=torch.float32))
+    with pytest.raises(ValueError):
+        qm.quantize_block(z(0, rows))
+    with pytest.raises(ValueError):
+        qm.swiglu_quantize_block(z(0, 2 * rows))
+
+
+def test_a_stream_of_another_device_is_refused():
+    class Stream:
+        device = torch.device("cuda", 1)
+    with pytest.raises(ValueError):
+        qm.quantize_block(torch.zeros(2, 128, device="cuda"), stream=Stream())
+
+
 # ------------------------------------------------------------------ streams, graphs, large offsets
 
 def _all(x, w, dy, off, perm, k, a, sa, wq, sw):
