@@ -10,9 +10,9 @@
 // maximum and the conversion, 16 elements per lane, so that a lane's codes
 // leave as one 16-byte store; memory bounds them. 32 x [2048][4096] bf16
 // weights in 128 x 128 blocks: 149 us, 5.4 TB/s (a large copy: 4.9). The
-// SwiGLU's sigmoid takes a reciprocal (at most 3 ulp from the division):
-// 24576 rows of 2048 43 us, 5.9 TB/s; with the division the VALU bounds it at
-// 55 us. One row of 4096: 7.2 us a call, the host's side of it.
+// SwiGLU divides by way of a reciprocal: 24576 rows of 2048 45 us, 5.7 TB/s;
+// with the division itself the VALU bounds it at 55 us. One row of 4096: 7.2
+// us a call, the host's side of it.
 #include "common.hpp"
 #include "kernels.hpp"
 
@@ -94,6 +94,17 @@ __device__ __forceinline__ uint4 to_codes(const float (&v)[16], float inv) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// z / (1 + e^-z), the quotient from a reciprocal and set right by its residual
+// (exact in one FMA): the division's own rounding but for the rarest near
+// ties. z = inf gives NaN for inf, which a block takes alike. Below z = -64,
+// where the reciprocal of 1 + e^-z would leave the normal range, the division.
+__device__ __forceinline__ float silu_quotient(float z) {
+  const float d = 1.0f + expf(-z);
+  if (z <= -64.0f) return z / d;
+  const float r = __builtin_amdgcn_rcpf(d), q = z * r;
+  return fmaf(fmaf(-d, q, z), r, q);
+}
+
 // Quantise one lane's part of a block whose maximum is `bits` on every lane.
 __device__ __forceinline__ uint4 finish(const float (&v)[16], uint32_t bits, int pow2, float* s, int32_t* err) {
   if (bits >= 0x7f800000u) {
@@ -126,7 +137,7 @@ __global__ __launch_bounds__(256) void k_quantize_rows(const typename Elem<DT>::
       load16<DT>(p, v);
       load16<DT>(p + cols, u);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = silu_fast(v[i]) * u[i];
+      for (int i = 0; i < 16; ++i) v[i] = silu_quotient(v[i]) * u[i];
     } else {
       load16<DT>(src + row * cols + c, v);
     }
