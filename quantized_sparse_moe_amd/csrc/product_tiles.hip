@@ -539,7 +539,7 @@ __global__ __launch_bounds__(256) void k_split_product(ProductArgs a, int run) {
 // take 0.39 (1.05 PFLOP/s) and storing 1.07 GB 0.19 (5.5 TB/s); the two barely
 // overlap, since a wave alone on its SIMD gains little while the other stores.
 // (256 x 256 tiles, one to a CU: 0.73 ms; 128 x 128, three: 0.69.) At 8192^3
-// 0.92 ms, 1.19 PFLOP/s.
+// 0.90 ms, 1.23 PFLOP/s.
 template <int TYPE, int BM, int BN, bool LOOKUP>
 __global__ __launch_bounds__(256, 2) void k_tile_dw(DwArgs a, int64_t pairs, int run) {
   constexpr int S = 3, BK = 32, NT = 256, WM = 2, WN = 2;
@@ -557,8 +557,10 @@ __global__ __launch_bounds__(256, 2) void k_tile_dw(DwArgs a, int64_t pairs, int
   const int rtiles = (a.N + BM - 1) / BM, ctiles = (a.K + BN - 1) / BN;
   const int e = static_cast<int>(pair / (static_cast<int64_t>(rtiles) * ctiles));
   const int at = static_cast<int>(pair - static_cast<int64_t>(e) * rtiles * ctiles);
-  const int band = at / (8 * ctiles), high = min(8, rtiles - 8 * band), rest = at - band * 8 * ctiles;
-  const int r0 = (8 * band + rest % high) * BM, c0 = rest / high * BN;
+  // bands of 4 row tiles: a run of 32 pairs is then a square of 1024 x 1024,
+  // which reads least (bands of 8: 579 against 572 us, 8192^3 915 against 896)
+  const int band = at / (4 * ctiles), high = min(4, rtiles - 4 * band), rest = at - band * 4 * ctiles;
+  const int r0 = (4 * band + rest % high) * BM, c0 = rest / high * BN;
   const int lo = n > 0 ? min(max(a.offsets[e], 0), n) : 0;
   const int count = n > 0 ? max(min(max(a.offsets[e + 1], 0), n) - lo, 0) : 0;
 
