@@ -489,9 +489,10 @@ __global__ __launch_bounds__(256) void k_split_product(ProductArgs a, int run) {
                 part = mma16<0>(e4m3_to_bf16x8(f.w[u][h][x], f.w[u][h][x + 1]),
                                 e4m3_to_bf16x8(f.r[u][v][h][x], f.r[u][v][h][x + 1]), part);
           } else {
-            part = mma_fp8(
-                __builtin_bit_cast(i32x8_t, __builtin_shufflevector(f.w[u][0], f.w[u][1], 0, 1, 2, 3, 4, 5, 6, 7)),
-                __builtin_bit_cast(i32x8_t, __builtin_shufflevector(f.r[u][v][0], f.r[u][v][1], 0, 1, 2, 3, 4, 5, 6, 7)));
+            const auto join = [](u32x4_t lo, u32x4_t hi) {
+              return __builtin_bit_cast(i32x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+            };
+            part = mma_fp8(join(f.w[u][0], f.w[u][1]), join(f.r[u][v][0], f.r[u][v][1]));
           }
 #pragma unroll
           for (int x = 0; x < 4; ++x) acc[v][x] = fmaf(part[x], f.s[u][v], acc[v][x]);
@@ -830,7 +831,9 @@ hipError_t pick_tiles(const ProductArgs& a, hipStream_t s) {
   // of the 256 CUs, and for buckets only while rows fill the tile; a grouped
   // product in few rounds of 128 x 256 tiles takes the 128 x 128 ones, which
   // ragged buckets spread better (fp16, 24 buckets of 84 rows: 39 against
-  // 55 us).
+  // 55 us), but not with 16-bit inputs and buckets about as high as a tile
+  // (bf16, 16 experts of 2048 x 2048, 192 rows each: 60 us against 66, 8 of
+  // 4096 x 2048, 160 each: 43 against 47; FP8: 40 against 36).
   if constexpr (!CT) {
     // 16 columns of split contraction. A round of 256 of its workgroups takes
     // 7 / 10 / 15 us for 16 / 32 / 64 rows (FP8, contraction 4096) where one of
@@ -853,7 +856,9 @@ hipError_t pick_tiles(const ProductArgs& a, hipStream_t s) {
     if (mean >= 192 && tiles(256, 256) >= 192) return launch_tiles<TYPE, 256, 256, 2, 4, 2, CT>(a, s);
   }
   if (mean >= 48) {
-    if (tiles(128, 256) >= (a.offsets ? 512 : 192)) return launch_tiles<TYPE, 128, 256, 2, 4, 3, CT>(a, s);
+    constexpr bool kFp8 = TYPE == kTypeE4m3 || TYPE == kE4m3Wide;
+    if (tiles(128, 256) >= (a.offsets && (kFp8 || mean < 120) ? 512 : 192))
+      return launch_tiles<TYPE, 128, 256, 2, 4, 3, CT>(a, s);
     if (tiles(128, 128) >= 256) return launch_tiles<TYPE, 128, 128, 2, 2, 2, CT>(a, s);
   }
   return launch_tiles<TYPE, 64, 128, 2, 2, 3, CT>(a, s);

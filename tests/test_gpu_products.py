@@ -161,7 +161,7 @@ def test_matmul_block(M, N, K, out):
 # Sizes that reach each tile size and the steps in the middle of a long contraction: rows x columns that fill the chip
 # with 256 x 256 tiles, with 128 x 256 (ragged and dense), with 128 x 128 and 64 x 128 ones. Columns, contraction, rows.
 FILL = [(4100, 1, 4, 4104, 528, "skew"), (2050, 3, 64, 2056, 656, "even"), (1000, 2, 16, 2056, 1296, "skew"),
-        (900, 4, 128, 1032, 400, "skew")]
+        (900, 4, 128, 1032, 400, "skew"), (800, 2, 16, 2056, 1296, "skew")]
 
 
 @pytest.mark.parametrize("T,k,E,C,Q,kind", FILL)
