@@ -33,6 +33,7 @@ MOE_DEVERR_QUANT_INPUT = 8
 MOE_DEVERR_ROW_INDEX = 16
 
 MOE_DT = {"bf16": 0, "f32": 1, "f16": 2}
+MOE_SUMS_F32 = 0x100
 MOE_ROWS = {"bucket": 0, "token": 1, "slot": 2}
 
 

@@ -414,6 +414,10 @@ def _out(out: Optional[torch.Tensor], shape, dtype: torch.dtype, device) -> torc
     return out
 
 
+def _block_out(y: torch.Tensor, f32_sums: bool) -> int:
+    return _DT[y.dtype] | (_lib.MOE_SUMS_F32 if f32_sums else 0)
+
+
 def _blocks(n: int) -> int:
     return -(-n // 128)
 
@@ -458,10 +462,13 @@ def swiglu_quantize_block(gu: torch.Tensor, pow2: bool = False, err: Optional[to
 
 
 def matmul_block(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scales: torch.Tensor,
-                 out_dtype: str = "bf16", out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                 out_dtype: str = "bf16", out: Optional[torch.Tensor] = None, stream=None,
+                 f32_sums: bool = False) -> torch.Tensor:
     """a @ b^T of block-scaled FP8 matrices (moe_matmul_block): a [M][K] with
     1 x 128 scales, b [N][K] with 128 x 128 scales -> [M][N]. A given `out`
-    decides the output type."""
+    decides the output type. A bf16 result is summed by the FP8 matrix
+    instruction, which drops the low bits of small products next to large ones;
+    `f32_sums` makes its sums fp32, as those of the other types always are."""
     dev = _operand(a, "a", _FP8, (2,)).device
     M, K = a.shape
     N = _operand(b, "b", _FP8, (2,), dev).shape[0]
@@ -471,10 +478,10 @@ def matmul_block(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_sca
     _shape(_operand(b_scales, "b_scales", _F32, (2,), dev), "b_scales", (_blocks(N), _blocks(K)))
     if _elsewhere(dev, stream):
         with _on(dev, stream):
-            return matmul_block(a, a_scales, b, b_scales, out_dtype, out)
+            return matmul_block(a, a_scales, b, b_scales, out_dtype, out, None, f32_sums)
     y = _out(out, (M, N), _out_type(out_dtype), dev)
     check(_lib.load().moe_matmul_block(a.data_ptr(), a_scales.data_ptr(), b.data_ptr(), b_scales.data_ptr(), M, N, K,
-                                       _DT[y.dtype], y.data_ptr(), _raw_stream(dev.index)), "moe_matmul_block")
+                                       _block_out(y, f32_sums), y.data_ptr(), _raw_stream(dev.index)), "moe_matmul_block")
     return y
 
 
@@ -499,12 +506,13 @@ def grouped_matmul_block(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tenso
                          offsets: torch.Tensor, perm: Optional[torch.Tensor] = None, top_k: int = 1,
                          x_order: str = "bucket", out_order: str = "bucket", out_dtype: str = "bf16",
                          out: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None,
-                         stream=None) -> torch.Tensor:
+                         stream=None, f32_sums: bool = False) -> torch.Tensor:
     """Rows grouped by expert times their expert's weights, block-scaled FP8
     (moe_grouped_matmul_block): a [rows][K] with 1 x 128 scales in `x_order`
     ("bucket", "token" or "slot"), w [E][N][K] with 128 x 128 scales, offsets
     and perm as `permute` gives them -> [T * top_k][N] in `out_order` ("bucket"
-    or "slot"). Rows of no bucket are not written."""
+    or "slot"). Rows of no bucket are not written. `f32_sums` as in
+    matmul_block."""
     dev = _operand(a, "a", _FP8, (2,)).device
     E, N, K = _operand(w, "w", _FP8, (3,), dev).shape
     rows = a.shape[0]
@@ -515,12 +523,12 @@ def grouped_matmul_block(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tenso
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return grouped_matmul_block(a, a_scales, w, w_scales, offsets, perm, top_k, x_order, out_order, out_dtype,
-                                        out, err)
+                                        out, err, None, f32_sums)
     y = _out(out, (T * top_k, N), _out_type(out_dtype), dev)
     check(_lib.load().moe_grouped_matmul_block(
         a.data_ptr(), a_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(), T, top_k, N, K, E, offsets.data_ptr(),
         None if perm is None else perm.data_ptr(), _lib.MOE_ROWS[x_order], _lib.MOE_ROWS.get(out_order, -1),
-        _DT[y.dtype], y.data_ptr(), _err_ptr(err, dev), _raw_stream(dev.index)), "moe_grouped_matmul_block")
+        _block_out(y, f32_sums), y.data_ptr(), _err_ptr(err, dev), _raw_stream(dev.index)), "moe_grouped_matmul_block")
     return y
 
 

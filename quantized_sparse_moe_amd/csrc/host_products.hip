@@ -19,6 +19,13 @@ moe_status hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_
 
 bool is_dtype(int32_t d) { return d == MOE_DT_BF16 || d == MOE_DT_F32 || d == MOE_DT_F16; }
 
+// out_dtype of the FP8 products: its flag and the type itself.
+int32_t take_f32_sums(int32_t* out_dtype) {
+  const int32_t flag = *out_dtype & MOE_SUMS_F32;
+  *out_dtype &= ~MOE_SUMS_F32;
+  return flag != 0;
+}
+
 // The kernels index one expert's tiles and all positions, rounded up to a
 // tile, with 32 bits.
 constexpr int32_t kMaxSide = 1 << 20, kMaxRows = 1 << 30;
@@ -72,6 +79,7 @@ moe_status moe_matmul_block(const uint8_t* a, const float* a_scales, const uint8
                             int32_t M, int32_t N, int32_t K, int32_t out_dtype, void* out, hipStream_t stream) {
   moe_status s = check_groups(M, 1, N, K, 1);
   if (s != MOE_OK) return s;
+  const int32_t f32_sums = take_f32_sums(&out_dtype);
   if (!is_dtype(out_dtype)) return MOE_ERR_INVALID_ARG;
   if (K % 16 != 0 || N % 8 != 0) return MOE_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return MOE_OK;
@@ -79,7 +87,7 @@ moe_status moe_matmul_block(const uint8_t* a, const float* a_scales, const uint8
     return MOE_ERR_INVALID_ARG;
   if (!aligned(a, 16) || !aligned(b, 16) || !aligned(out, 16) || !aligned(a_scales, 4) || !aligned(b_scales, 4))
     return MOE_ERR_ALIGNMENT;
-  ProductArgs p{a, a_scales, b, b_scales, kTypeE4m3, out_dtype, M, 1, 1, N, K, 0, nullptr, nullptr,
+  ProductArgs p{a, a_scales, b, b_scales, kTypeE4m3, out_dtype, M, 1, 1, N, K, 0, f32_sums, nullptr, nullptr,
                 MOE_ROWS_BUCKET, MOE_ROWS_BUCKET, out, nullptr};
   const hipError_t e = launch_product(p, stream);
   return e == hipErrorInvalidValue ? MOE_ERR_UNSUPPORTED : hip_status(e);
@@ -91,6 +99,7 @@ moe_status moe_grouped_matmul_block(const uint8_t* a, const float* a_scales, con
                                     void* out, int32_t* err, hipStream_t stream) {
   moe_status s = check_groups(T, k, N, K, E);
   if (s != MOE_OK) return s;
+  const int32_t f32_sums = take_f32_sums(&out_dtype);
   if (!is_dtype(out_dtype)) return MOE_ERR_INVALID_ARG;
   if (K % 16 != 0 || N % 8 != 0) return MOE_ERR_UNSUPPORTED;
   if ((s = check_orders(a_order, out_order, true, T > 0 ? perm : reinterpret_cast<const int32_t*>(4))) != MOE_OK)
@@ -102,8 +111,8 @@ moe_status moe_grouped_matmul_block(const uint8_t* a, const float* a_scales, con
   if (!aligned(a, 16) || !aligned(w, 16) || !aligned(out, 16) || !aligned(a_scales, 4) || !aligned(w_scales, 4) ||
       !aligned(offsets, 4) || !aligned(perm, 4) || !aligned(err, 4))
     return MOE_ERR_ALIGNMENT;
-  ProductArgs p{a, a_scales, w, w_scales, kTypeE4m3, out_dtype, T, k, E, N, K, 0, offsets, perm, a_order, out_order,
-                out, err};
+  ProductArgs p{a, a_scales, w, w_scales, kTypeE4m3, out_dtype, T, k, E, N, K, 0, f32_sums, offsets, perm, a_order,
+                out_order, out, err};
   const hipError_t e = launch_product(p, stream);
   return e == hipErrorInvalidValue ? MOE_ERR_UNSUPPORTED : hip_status(e);
 }
@@ -124,7 +133,7 @@ moe_status moe_grouped_matmul(const void* x, const void* w, int32_t dtype, int32
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(out, 16) || !aligned(offsets, 4) || !aligned(perm, 4) ||
       !aligned(err, 4))
     return MOE_ERR_ALIGNMENT;
-  ProductArgs p{x, nullptr, w, nullptr, dtype, out_dtype, T, k, E, C, Q, transposed != 0, offsets, perm, x_order,
+  ProductArgs p{x, nullptr, w, nullptr, dtype, out_dtype, T, k, E, C, Q, transposed != 0, 0, offsets, perm, x_order,
                 out_order, out, err};
   const hipError_t e = launch_product(p, stream);
   return e == hipErrorInvalidValue ? MOE_ERR_UNSUPPORTED : hip_status(e);

@@ -162,6 +162,7 @@ struct ProductArgs {
   int32_t T, k, E;
   int32_t C, Q;            // output columns, contraction length
   int32_t transposed;
+  int32_t f32_sums;        // e4m3 with a bf16 output: fp32 sums there too
   const int32_t* offsets;  // null: one expert for all rows
   const int32_t* perm;
   int32_t r_order, out_order;

@@ -102,13 +102,19 @@ __device__ __forceinline__ f32x4_t mma16(u32x4_t a, u32x4_t b, f32x4_t c) {
 // 16 x 16 x 128 over E4M3 from zero; the unscaled form (scales 0). The
 // instruction sums 8 neighbouring products at a time on the exponent of the
 // largest and drops what lies more than 13 bits below it (measured: a second
-// product is exact down to 2^-13 of the first, changed from 2^-14 on; groups
-// of 8 are then summed in fp32). That error, at most 7 * 2^-13 of the largest
-// product of a group and 2e-5 of the result in the norm (4096 inputs; fp16
-// outputs are 2.084e-4 off the fp32 sums, which rounding alone makes 2.075e-4,
-// bf16 ones 1.6595e-3 and 1.6594e-3), is below the rounding of a 16-bit
-// output; fp32 outputs go through bf16 instead, where every product is exact
-// and sums are fp32.
+// product is exact down to 2^-13 of the first, changed from 2^-14 on, and lost
+// too where the largest products cancel; groups of 8 are then summed in fp32).
+// The error is at most 7 * 2^-13 of the largest product of a group. Measured
+// over blocks of 128, as a share of the result in the norm: normal inputs
+// 1.3e-5, inputs of one sign 3.0e-6 (2.4e-6 of it towards zero), channels
+// scaled by e^(2 z) 5.3e-5, the largest error of one result 1.9e-4 of its sum
+// of |products|. Rounding to bf16 is 1.66e-3 in the norm, 30 times the worst of
+// these, so bf16 outputs are formed this way unless the caller asks for fp32
+// sums (their error against 64 bits is 1.6595e-3, of which rounding alone makes
+// 1.6594e-3). Rounding to fp16, 2.1e-4, is not far enough above it: fp16 and
+// fp32 outputs go through bf16, where every product is exact and sums are fp32
+// (1e-8 to 4e-8 in the same three norms). The K = 32 FP8 instruction drops the
+// same bits.
 __device__ __forceinline__ f32x4_t mma_fp8(i32x8_t a, i32x8_t b) {
   const f32x4_t z = {0.0f, 0.0f, 0.0f, 0.0f};
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, z, 0, 0, 0, 0, 0, 0);

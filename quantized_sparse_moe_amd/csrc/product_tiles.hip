@@ -47,7 +47,7 @@ __device__ __forceinline__ int swz_c(int n) { return (n & 3) | (((n >> 4) & 1) <
 // contraction-major: XOR of the 16-byte piece index, even values
 __device__ __forceinline__ int swz_q(int q) { return ((q & 3) | (((q >> 3) & 1) << 2)) << 1; }
 
-constexpr int kE4m3Wide = 4;  // E4M3 multiplied as bf16 (fp32 outputs)
+constexpr int kE4m3Wide = 4;  // E4M3 multiplied as bf16: exact products, fp32 sums
 
 template <int TYPE, int BM, int BN, int WM, int WN, int S, bool CT>
 __global__ __launch_bounds__(WM* WN * 64) void k_tile_product(ProductArgs a, int run) {
@@ -902,7 +902,7 @@ hipError_t pick_dw(DwArgs a, hipStream_t s) {
 
 hipError_t launch_product(const ProductArgs& a, hipStream_t s) {
   if (a.type == kTypeE4m3)
-    return a.out_type == 1 ? pick_tiles<kE4m3Wide, false>(a, s) : pick_tiles<kTypeE4m3, false>(a, s);
+    return a.out_type != 0 || a.f32_sums ? pick_tiles<kE4m3Wide, false>(a, s) : pick_tiles<kTypeE4m3, false>(a, s);
   if (a.type == 0) return a.transposed ? pick_tiles<0, true>(a, s) : pick_tiles<0, false>(a, s);
   return a.transposed ? pick_tiles<2, true>(a, s) : pick_tiles<2, false>(a, s);
 }

@@ -136,3 +136,13 @@ def test_python_calls_refuse_host_tensors_types_and_shapes():
         qm.grouped_matmul(x.float(), w.float(), off)
     with pytest.raises(TypeError):
         qm.matmul_block(x, s, q, s)
+
+
+def test_f32_sums_is_a_flag_of_the_fp8_products():
+    S = _lib.MOE_SUMS_F32
+    for dt in _lib.MOE_DT.values():
+        assert dense(M=0, out_dtype=dt | S) == OK and grouped_block(N=0, out_dtype=dt | S) == OK
+    for call in (dense, grouped_block):
+        for bad in (3 | S, S << 1, -1):
+            assert call(out_dtype=bad) == INVALID
+    assert grouped(out_dtype=S) == INVALID and grouped_dw(out_dtype=1 | S) == INVALID
