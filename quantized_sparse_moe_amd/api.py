@@ -371,6 +371,14 @@ def _operand(t: torch.Tensor, name: str, dtypes, dims, device=None) -> torch.Ten
     return t
 
 
+def _unrecorded(call: str) -> None:
+    """Refuse a product that autograd would have to record: its result would
+    look like a constant, and the operands' gradients would be lost in silence."""
+    if torch.is_grad_enabled():
+        raise RuntimeError(f"{call} is not recorded by autograd, but an operand requires grad: call it under "
+                           "torch.no_grad(), with detached operands, or inside a torch.autograd.Function")
+
+
 def _shape(t: torch.Tensor, name: str, shape) -> None:
     if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -426,7 +434,8 @@ def quantize_block(x: torch.Tensor, block_rows: int = 1, pow2: bool = False, err
                    stream=None):
     """E4M3 codes with an fp32 scale per block of `block_rows` (1 or 128) rows
     and 128 columns (moe_quantize_block): x bf16, fp16 or fp32 [rows][cols], or
-    [matrices][rows][cols] -> (codes float8_e4m3fn of x's shape, scales)."""
+    [matrices][rows][cols] -> (codes float8_e4m3fn of x's shape, scales). A
+    quantised copy: codes and scales are constants to autograd."""
     dev = _operand(x, "x", _DT, (2, 3)).device
     if _elsewhere(dev, stream):
         with _on(dev, stream):
@@ -443,7 +452,8 @@ def quantize_block(x: torch.Tensor, block_rows: int = 1, pow2: bool = False, err
 
 def swiglu_quantize_block(gu: torch.Tensor, pow2: bool = False, err: Optional[torch.Tensor] = None, stream=None):
     """silu(gate) * up of gu [rows][gate | up], quantised per 1 x 128 block
-    (moe_swiglu_quantize_block) -> (codes [rows][inner], scales)."""
+    (moe_swiglu_quantize_block) -> (codes [rows][inner], scales), constants to
+    autograd."""
     dev = _operand(gu, "gu", _DT, (2,)).device
     if _elsewhere(dev, stream):
         with _on(dev, stream):
@@ -468,7 +478,10 @@ def matmul_block(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_sca
     1 x 128 scales, b [N][K] with 128 x 128 scales -> [M][N]. A given `out`
     decides the output type. A bf16 result is summed by the FP8 matrix
     instruction, which drops the low bits of small products next to large ones;
-    `f32_sums` makes its sums fp32, as those of the other types always are."""
+    `f32_sums` makes its sums fp32, as those of the other types always are.
+    Not recorded by autograd: operands that require grad are refused."""
+    if a.requires_grad or a_scales.requires_grad or b.requires_grad or b_scales.requires_grad:
+        _unrecorded("matmul_block")
     dev = _operand(a, "a", _FP8, (2,)).device
     M, K = a.shape
     N = _operand(b, "b", _FP8, (2,), dev).shape[0]
@@ -511,8 +524,10 @@ def grouped_matmul_block(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tenso
     (moe_grouped_matmul_block): a [rows][K] with 1 x 128 scales in `x_order`
     ("bucket", "token" or "slot"), w [E][N][K] with 128 x 128 scales, offsets
     and perm as `permute` gives them -> [T * top_k][N] in `out_order` ("bucket"
-    or "slot"). Rows of no bucket are not written. `f32_sums` as in
-    matmul_block."""
+    or "slot"). Rows of no bucket are not written. `f32_sums` and operands that
+    require grad as in matmul_block."""
+    if a.requires_grad or a_scales.requires_grad or w.requires_grad or w_scales.requires_grad:
+        _unrecorded("grouped_matmul_block")
     dev = _operand(a, "a", _FP8, (2,)).device
     E, N, K = _operand(w, "w", _FP8, (3,), dev).shape
     rows = a.shape[0]
@@ -540,7 +555,11 @@ def grouped_matmul(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, perm
     (moe_grouped_matmul): w [E][N][K]; y = x w^T, or with `transposed` y = x w
     (the gradient in the rows of a product with w^T). Orders as in
     grouped_matmul_block; the output type is x's unless `out_dtype` or `out`
-    says otherwise."""
+    says otherwise. Not recorded by autograd (operands that require grad are
+    refused): the gradients are this call with `transposed` and
+    grouped_matmul_dw."""
+    if x.requires_grad or w.requires_grad:
+        _unrecorded("grouped_matmul")
     dev = _operand(x, "x", _B16, (2,)).device
     E, N, K = _operand(w, "w", (x.dtype,), (3,), dev).shape
     rows = x.shape[0]
@@ -564,7 +583,10 @@ def grouped_matmul_dw(x: torch.Tensor, dy: torch.Tensor, offsets: torch.Tensor, 
                       stream=None) -> torch.Tensor:
     """The gradient of grouped_matmul in the weights (moe_grouped_matmul_dw):
     x [rows][K] in `x_order`, dy [T * top_k][N] in `dy_order` ("bucket" or
-    "slot") -> [E][N][K], the sum over each expert's positions of dy x^T."""
+    "slot") -> [E][N][K], the sum over each expert's positions of dy x^T. Not
+    recorded by autograd either."""
+    if x.requires_grad or dy.requires_grad:
+        _unrecorded("grouped_matmul_dw")
     dev = _operand(x, "x", _B16, (2,)).device
     rows, K = x.shape
     N = _operand(dy, "dy", (x.dtype,), (2,), dev).shape[1]

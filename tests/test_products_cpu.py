@@ -146,3 +146,31 @@ def test_f32_sums_is_a_flag_of_the_fp8_products():
         for bad in (3 | S, S << 1, -1):
             assert call(out_dtype=bad) == INVALID
     assert grouped(out_dtype=S) == INVALID and grouped_dw(out_dtype=1 | S) == INVALID
+
+
+def test_products_refuse_operands_that_require_grad():
+    """autograd does not record these calls: a result without a grad_fn would lose the gradients in silence. Under
+    no_grad and inside an autograd.Function the calls go on (here to the refusal of host tensors)."""
+    x, w, dy = torch.zeros(4, 16), torch.zeros(2, 8, 16), torch.zeros(4, 8)
+    x, w, dy = (t.bfloat16() for t in (x, w, dy))
+    off = torch.zeros(3, dtype=torch.int32)
+    q, s = torch.zeros(4, 16, dtype=torch.uint8), torch.zeros(4, 1)
+    g = lambda t: t.clone().requires_grad_()  # noqa: E731
+    calls = [lambda: qm.grouped_matmul(g(x), w, off), lambda: qm.grouped_matmul(x, g(w), off),
+             lambda: qm.grouped_matmul(dy, g(w), off, transposed=True),
+             lambda: qm.grouped_matmul_dw(g(x), dy, off), lambda: qm.grouped_matmul_dw(x, g(dy), off),
+             lambda: qm.matmul_block(q, g(s), q, s), lambda: qm.matmul_block(q, s, q, g(s)),
+             lambda: qm.grouped_matmul_block(q, g(s), q[None], s[None], off),
+             lambda: qm.grouped_matmul_block(q, s, q[None], g(s[None]), off)]
+    for call in calls:
+        with pytest.raises(RuntimeError, match="not recorded by autograd"):
+            call()
+        with torch.no_grad(), pytest.raises(ValueError, match="contiguous device tensor"):
+            call()
+
+    class Product(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, w):
+            return qm.grouped_matmul(x, w, off)
+    with pytest.raises(ValueError, match="contiguous device tensor"):
+        Product.apply(g(x), g(w))
