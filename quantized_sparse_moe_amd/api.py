@@ -92,23 +92,34 @@ class DeviceExperts:
 
 
 class DeviceLayer:
-    """Router, routed experts and optional shared expert of one MoE layer."""
+    """Router, routed experts and optional shared expert of one MoE layer. With
+    `routed` None it is a router alone, for experts that the layer's packed
+    formats do not hold (the grouped products): router_logits, route and
+    workspace take it, the calls that run experts refuse it."""
 
     def __init__(self, route: str, top_k: int, wr: torch.Tensor, bias: Optional[torch.Tensor],
-                 tid2eid: Optional[torch.Tensor], routed: DeviceExperts, shared: Optional[DeviceExperts],
-                 routed_scale: float = 1.0):
+                 tid2eid: Optional[torch.Tensor], routed: Optional[DeviceExperts] = None,
+                 shared: Optional[DeviceExperts] = None, routed_scale: float = 1.0):
+        if routed is None and shared is not None:
+            raise ValueError("a shared expert needs routed experts beside it")
         self.route, self.top_k = route, top_k
         self.wr, self.bias, self.tid2eid = wr, bias, tid2eid
         self.routed, self.shared = routed, shared
         self.E, self.d = wr.shape
-        self.I = routed.gate.rows
+        self.I = 0 if routed is None else routed.gate.rows
         self.vocab = 0 if tid2eid is None else tid2eid.shape[0]
         self.router_c = RouterC(_lib.MOE_ROUTE_HASH if route == "hash" else _lib.MOE_ROUTE_TOPK, self.E, top_k,
                                 self.d, self.vocab, wr.data_ptr(), bias.data_ptr() if bias is not None else None,
                                 tid2eid.data_ptr() if tid2eid is not None else None, routed_scale)
         self._shared_c = shared.c if shared is not None else None
-        self.c = LayerC(self.router_c, routed.c,
-                        ctypes.pointer(self._shared_c) if shared is not None else ctypes.POINTER(ExpertsC)())
+        self._c = None if routed is None else LayerC(
+            self.router_c, routed.c, ctypes.pointer(self._shared_c) if shared is not None else ctypes.POINTER(ExpertsC)())
+
+    @property
+    def c(self) -> LayerC:
+        if self._c is None:
+            raise ValueError("this layer is a router without packed experts")
+        return self._c
 
     @classmethod
     def from_host(cls, layer, device="cuda", routed=None) -> "DeviceLayer":
@@ -123,11 +134,16 @@ class DeviceLayer:
     def clone(self) -> "DeviceLayer":
         """An independent device copy of every weight (same values, new memory)."""
         c = lambda t: None if t is None else t.clone()
-        return DeviceLayer(self.route, self.top_k, c(self.wr), c(self.bias), c(self.tid2eid), self.routed.clone(),
-                           None if self.shared is None else self.shared.clone(), self.router_c.routed_scale)
+        return DeviceLayer(self.route, self.top_k, c(self.wr), c(self.bias), c(self.tid2eid), c(self.routed),
+                           c(self.shared), self.router_c.routed_scale)
 
     # -- workspace ---------------------------------------------------------
     def workspace_size(self, max_tokens: int) -> int:
+        if self._c is None:  # what moe_route needs by its documentation; moe_permute needs the first 256 bytes
+            if max_tokens < 0:
+                raise _lib.MoeError(_lib.MOE_ERR_INVALID_ARG, "workspace_size")
+            words = 4 * max_tokens * self.E if self.route == "topk" else 0
+            return 256 + sum(-(-n // 256) * 256 for n in (words, 2 * words, words))
         n = _lib.load().moe_workspace_size(ctypes.byref(self.c), max_tokens)
         if n == 0:
             raise _lib.MoeError(_lib.MOE_ERR_INVALID_ARG, "moe_workspace_size")
@@ -217,6 +233,8 @@ def permute(ids: torch.Tensor, num_experts: int, ws: torch.Tensor, stream=None):
 
 def expert_ffn(layer: DeviceLayer, x: torch.Tensor, offsets: torch.Tensor, perm: torch.Tensor,
                ws: torch.Tensor, stream=None):
+    if layer.routed is None:
+        raise ValueError("this layer is a router without packed experts")
     x = _bits_tensor(x)
     T, k, d = x.shape[0], layer.top_k, layer.d
     y_slot = torch.empty((T * k, d), dtype=torch.float32, device=x.device)

@@ -174,3 +174,28 @@ def test_products_refuse_operands_that_require_grad():
             return qm.grouped_matmul(x, w, off)
     with pytest.raises(ValueError, match="contiguous device tensor"):
         Product.apply(g(x), g(w))
+
+
+@pytest.mark.parametrize("route", ["topk", "hash"])
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 256, 6), (7, 33, 2), (300, 1000, 8)])
+def test_a_router_without_packed_experts_sizes_its_workspace(route, T, E, k):
+    """The size is what moe_route asks for: with a byte less it refuses the workspace, with all of them it comes to the
+    next check (a misaligned one)."""
+    wr, table = torch.zeros(E, 64), torch.zeros(10, k, dtype=torch.int32)
+    layer = qm.DeviceLayer(route, k, wr, None, table if route == "hash" else None)
+    n = layer.workspace_size(T)
+    call = lambda ws, size: qm.load().moe_route(layer.router_c, F, F, T, F, F, ws, size, None)  # noqa: E731
+    assert call(F, n - 1) == _lib.MOE_ERR_WORKSPACE and call(F + 64, n) == ALIGNMENT
+    assert layer.workspace_size(0) >= 256 and layer.I == 0 and layer.clone().workspace_size(T) == n
+    with pytest.raises(_lib.MoeError):
+        layer.workspace_size(-1)
+
+
+def test_a_router_without_packed_experts_is_refused_where_experts_run():
+    layer = qm.DeviceLayer("topk", 2, torch.zeros(4, 64), None, None)
+    x = torch.zeros(3, 64, dtype=torch.bfloat16)
+    for call in (lambda: layer.workspace_layout(3), lambda: layer.c, lambda: qm.expert_ffn(layer, x, x, x, x)):
+        with pytest.raises(ValueError, match="router without packed experts"):
+            call()
+    with pytest.raises(ValueError, match="needs routed experts"):
+        qm.DeviceLayer("topk", 2, torch.zeros(4, 64), None, None, None, object())
