@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import oracle
+from tests._quant import check_swiglu
 
 
 def test_e4m3_encode_inverts_decode_and_rounds_to_even():
@@ -68,3 +69,46 @@ def test_grouped_products_against_loops_and_differences():
         assert np.isclose(((oracle.grouped_matmul(x, w + tw, off)[0] - y) * dy).sum(), (dw * tw).sum())
         assert np.isclose(((oracle.grouped_matmul(x + tx, w, off)[0] - y) * dy).sum(), (dx * tx).sum())
     assert not dw[1].any()
+
+
+def _swiglu_inputs(rows, inner, seed):
+    rng = np.random.default_rng(seed)
+    return (rng.standard_normal((rows, 2 * inner)) * np.exp(rng.standard_normal(2 * inner))).astype(np.float32)
+
+
+@pytest.mark.parametrize("pow2", [False, True])
+@pytest.mark.parametrize("rows,inner", [(1, 16), (6, 2048), (33, 272)])
+def test_swiglu_check_accepts_the_oracle_and_refuses_mistakes(rows, inner, pow2):
+    """The value-by-value check of the SwiGLU quantiser: scales off by a factor of two (with any codes), other codes,
+    a few flipped signs or codes one step away are all refused."""
+    gu = _swiglu_inputs(rows, inner, rows)
+    codes, scales = oracle.swiglu_quantize_block(gu, pow2)
+    check_swiglu(codes, scales, gu, pow2)
+    rng = np.random.default_rng(1)
+    big = np.argmax(np.abs(codes.astype(int) & 127))
+    flipped, stepped = codes.copy(), codes.copy()
+    flipped.flat[big] ^= 0x80
+    stepped.flat[big] -= 1
+    one_block = scales.copy()
+    one_block[0, 0] *= 2
+    wrong = [(np.zeros_like(codes), scales * 2), (codes, scales * 2), (codes, scales / 2), (codes, one_block),
+             (rng.integers(0, 127, codes.shape).astype(np.uint8), scales / 2), (flipped, scales), (stepped, scales),
+             (np.zeros_like(codes), scales), (codes, scales * np.float32(1 + 2.0 ** -18))]
+    for c, s in wrong:
+        with pytest.raises(AssertionError):
+            check_swiglu(c, s, gu, pow2)
+
+
+def test_swiglu_check_allows_a_power_of_two_only_where_it_is_near():
+    """amax / 448 a power of two up to the last bits: either scale is right, with its own codes; a code on a boundary
+    may be either neighbour."""
+    gu = np.zeros((1, 32), np.float32)
+    gu[0, :16], gu[0, 16:] = 60.0, np.arange(16) / 60         # silu(60) = 60 but for e^-60
+    gu[0, 31] = np.float32(448) / np.float32(60)              # 448 up to a rounding
+    codes, scales = oracle.swiglu_quantize_block(gu, True)
+    check_swiglu(codes, scales, gu, True)
+    h = (gu[0, :16] * gu[0, 16:]).astype(np.float64)
+    for s in (1.0, 2.0):
+        check_swiglu(oracle.e4m3_encode(np.clip(h / s, -448, 448))[None], np.full((1, 1), s, np.float32), gu, True)
+    with pytest.raises(AssertionError):
+        check_swiglu(oracle.e4m3_encode(h / 4)[None], np.full((1, 1), 4.0, np.float32), gu, True)
