@@ -453,11 +453,13 @@ moe_status moe_matmul_block(const uint8_t* a, const float* a_scales, const uint8
  * offsets[e+1] - 1 use expert e's weights. An expert may have no position;
  * positions outside every bucket (before offsets[0], from offsets[E] on) are
  * neither read nor written, so their output rows stay as they were. Offsets
- * are clamped to [0, T*k], and buckets that do not ascend count as empty. A
- * perm entry outside [0, T*k) sets MOE_DEVERR_ROW_INDEX in *err (device int32
- * or NULL); some row of the matrix is read in its place, and an output row that
- * it would name is not written. perm may be NULL when no matrix is in token or
- * slot order; it must not name an output row twice.
+ * are clamped to [0, T*k], and a bucket that runs backwards counts as empty;
+ * where buckets overlap for that reason, their common positions get the result
+ * of one of them or none. A perm entry outside [0, T*k) sets
+ * MOE_DEVERR_ROW_INDEX in *err (device int32 or NULL); some row of the matrix
+ * is read in its place, and an output row that it would name is not written.
+ * perm may be NULL when no matrix is in token or slot order; it must not name
+ * an output row twice.
  *
  * moe_grouped_matmul_block: out[p][n] = sum_k a[p][k] * w[e(p)][n][k] over
  * block-scaled FP8, as moe_matmul_block: a in a_order, w [E][N][K], w_scales

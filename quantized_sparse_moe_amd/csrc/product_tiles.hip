@@ -72,7 +72,7 @@ __global__ __launch_bounds__(WM* WN * 64) void k_tile_product(ProductArgs a, int
   const int wm = wave / WN, wn = wave % WN;
   const int g = lane >> 4, j = lane & 15;
   const int c0 = t.ctile * BN;
-  const int qbytes = a.Q * ESIZE;  // < 2^21
+  const int qbytes = a.Q * ESIZE;  // <= 2^21
   const int steps = (qbytes + kStepBytes - 1) / kStepBytes;
   const int full = qbytes / kStepBytes;
   const int qb = (a.Q + 127) / 128;

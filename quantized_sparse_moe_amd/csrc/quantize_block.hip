@@ -122,9 +122,9 @@ __global__ __launch_bounds__(256) void k_quantize_rows(const typename Elem<DT>::
                                                        int cols, int pow2, uint8_t* __restrict__ codes,
                                                        float* __restrict__ scales, int32_t* err) {
   const int nb = (cols + 127) / 128;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x / 8;  // block of 128
-  const int64_t row = unit < INT32_MAX ? static_cast<uint32_t>(unit) / static_cast<uint32_t>(nb) : unit / nb;
-  const int b = static_cast<int>(unit - row * nb);
+  const uint32_t unit = blockIdx.x * 32 + threadIdx.x / 8;  // block of 128; a grid holds fewer than 2^24 workgroups
+  const int64_t row = unit / static_cast<uint32_t>(nb);
+  const int b = static_cast<int>(unit % static_cast<uint32_t>(nb));
   const int c = b * 128 + (threadIdx.x & 7) * 16;
   const bool valid = row < rows && c < cols;  // the lanes past the end stay in the shuffles
   float v[16];
