@@ -20,6 +20,9 @@ namespace qsmoe {
 
 namespace {
 
+// Blocks of 128 in a row; cols + 127 may pass 32 bits.
+__host__ __device__ constexpr int blocks_of(int cols) { return cols / 128 + (cols % 128 != 0); }
+
 constexpr int kDtBf16 = 0, kDtF32 = 1;  // moe_dtype; the third is fp16
 
 template <int DT>
@@ -121,7 +124,7 @@ template <int DT, bool SWIGLU>
 __global__ __launch_bounds__(256) void k_quantize_rows(const typename Elem<DT>::type* __restrict__ src, int64_t rows,
                                                        int cols, int pow2, uint8_t* __restrict__ codes,
                                                        float* __restrict__ scales, int32_t* err) {
-  const int nb = (cols + 127) / 128;
+  const int nb = blocks_of(cols);
   const uint32_t unit = blockIdx.x * 32 + threadIdx.x / 8;  // block of 128; a grid holds fewer than 2^24 workgroups
   const int64_t row = unit / static_cast<uint32_t>(nb);
   const int b = static_cast<int>(unit % static_cast<uint32_t>(nb));
@@ -159,7 +162,7 @@ __global__ __launch_bounds__(256) void k_quantize_tiles(const typename Elem<DT>:
                                                         uint8_t* __restrict__ codes, float* __restrict__ scales,
                                                         int32_t* err) {
   __shared__ uint32_t s_max[4];
-  const int nb = (cols + 127) / 128;
+  const int nb = blocks_of(cols);
   const int64_t tile = blockIdx.x;
   const int64_t mr = tile / nb;  // matrix * row_blocks + row block
   const int64_t m = mr / row_blocks;
@@ -193,7 +196,7 @@ __global__ __launch_bounds__(256) void k_quantize_tiles(const typename Elem<DT>:
 template <int DT, bool SWIGLU>
 hipError_t launch_rows(const void* x, int64_t rows, int cols, int pow2, uint8_t* codes, float* scales, int32_t* err,
                        hipStream_t s) {
-  const int64_t groups = (rows * ((cols + 127) / 128) + 31) / 32;
+  const int64_t groups = (rows * blocks_of(cols) + 31) / 32;
   if (groups > max_workgroups(256)) return hipErrorInvalidValue;
   QSMOE_LAUNCH((k_quantize_rows<DT, SWIGLU>), dim3(static_cast<unsigned>(groups)), dim3(256), 0, s,
                static_cast<const typename Elem<DT>::type*>(x), rows, cols, pow2, codes, scales, err);
@@ -203,7 +206,7 @@ hipError_t launch_rows(const void* x, int64_t rows, int cols, int pow2, uint8_t*
 template <int DT>
 hipError_t launch_tiles(const void* x, int64_t matrices, int64_t rows, int cols, int pow2, uint8_t* codes,
                         float* scales, int32_t* err, hipStream_t s) {
-  const int64_t rb = (rows + 127) / 128, nb = (cols + 127) / 128;
+  const int64_t rb = (rows + 127) / 128, nb = blocks_of(cols);
   constexpr int64_t most = max_workgroups(256);
   if (matrices > most / rb || matrices * rb > most / nb) return hipErrorInvalidValue;
   QSMOE_LAUNCH((k_quantize_tiles<DT>), dim3(static_cast<unsigned>(matrices * rb * nb)), dim3(256), 0, s,

@@ -199,3 +199,11 @@ def test_a_router_without_packed_experts_is_refused_where_experts_run():
             call()
     with pytest.raises(ValueError, match="needs routed experts"):
         qm.DeviceLayer("topk", 2, torch.zeros(4, 64), None, None, None, object())
+
+
+@pytest.mark.parametrize("cols", [(1 << 31) - 16, (1 << 31) - 112, (1 << 31) - 128])
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantize_block_counts_the_blocks_of_the_longest_rows(cols, block_rows):
+    """2^24 blocks in a row (one fewer for the last size): 64 rows of them are more workgroups than a grid holds, and a
+    count that wraps would not say so."""
+    assert quant(cols=cols, block_rows=block_rows, rows=64 if block_rows == 1 else 257) == UNSUPPORTED
