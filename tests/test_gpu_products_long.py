@@ -131,3 +131,18 @@ def test_subnormal_codes(M, N, K, out):
     want = torch.from_numpy(a @ b.T).to(DT[out])
     assert torch.equal(qm.matmul_block(code(a, 2.0 ** -9), sa, code(b, 1.0), sb, out_dtype=out).cpu(), want)
     assert torch.equal(qm.matmul_block(code(a, 1.0), sa, code(b, 2.0 ** -9), sb, out_dtype=out).cpu(), want)
+
+
+@pytest.mark.parametrize("M,N,K", [(2, 40, 144), (300, 4104, 272), (2100, 4096, 144)])
+@pytest.mark.parametrize("out,tiny", [("f16", 2.0 ** -24), ("bf16", 2.0 ** -133)])
+def test_subnormal_results(M, N, K, out, tiny):
+    """Integers up to 2 with scales that make every result a multiple of a quarter of the smallest subnormal: rounded
+    once, ties to even, as the reference's conversion from 64 bits does (through fp32, which holds them exactly)."""
+    rng = np.random.default_rng(N)
+    a, b = ints(rng, M, K), ints(rng, N, K)
+    code = lambda v: torch.from_numpy(v).to(torch.float8_e4m3fn).cuda()  # noqa: E731
+    sa = torch.full((M, -(-K // 128)), 2.0 ** -20).cuda()
+    sb = torch.full((-(-N // 128), -(-K // 128)), tiny / 4 * 2.0 ** 20).cuda()
+    want = (torch.from_numpy(a @ b.T).double() * tiny / 4).float().to(DT[out])
+    assert torch.equal(qm.matmul_block(code(a), sa, code(b), sb, out_dtype=out).cpu(), want)
+    assert (want.double().abs() == tiny).any()
