@@ -30,7 +30,12 @@
 //     TB/s of weights, rows and results, 87 % of the copy's rate; a tile's
 //     beginning and end (8 us of 48) is what is left. bf16, 2048 x 4096: 0.86
 //     ms, 5.1 TB/s.
-//   64 x 128, 512 tokens: 0.75 ms, 5.7 TB/s of weights.
+//   64 x 128, 512 tokens: 0.75 to 0.77 ms, 5.6 TB/s of weights.
+// E4M3 multiplied as bf16 (fp32 and fp16 outputs, fp32 sums) takes half the
+// matrix rate and converts its codes on the way: 4096 rows by 4096 x 4096 134
+// us against 72, 512 rows 31 against 19, 24576 rows over 256 experts of 4096 x
+// 2048 with fp32 outputs in slot order 0.75 ms (3.5 TB/s), 512 tokens 0.46 ms
+// (4.8 TB/s).
 #include <algorithm>
 #include <type_traits>
 
@@ -410,9 +415,11 @@ __global__ __launch_bounds__(WM* WN * 64) void k_tile_product(ProductArgs a, int
 // tiles the latency of doing so. A workgroup takes 16 RT rows and 16 columns of
 // one expert and its 4 waves every fourth step of the contraction each, weights
 // and rows straight from memory into registers, a group of steps ahead; their
-// sums meet in LDS in a fixed order. One FP8 row by 4096 x 4096: 7.4 us a call,
-// which the host's side of it bounds (64 x 128 tiles: 17.5 us); six of 256
-// experts, 100 MB: 20.4 us, 4.9 TB/s.
+// sums meet in LDS in a fixed order. One FP8 row by 4096 x 4096: 7.0 us a call,
+// which the host's side of it bounds, with one weight again and again or 24 in
+// turn (64 x 128 tiles: 17.5 us); six of 256 experts, 101 MB: 23.6 us, 4.3 TB/s
+// with other experts in every call, 20.3 us while the last-level cache holds
+// the same six.
 template <int TYPE, int RT>
 __global__ __launch_bounds__(256) void k_split_product(ProductArgs a, int run) {
   constexpr bool FP8 = TYPE == kTypeE4m3 || TYPE == kE4m3Wide;
@@ -893,6 +900,11 @@ void set_divisor(DwArgs& a) {
 template <int TYPE>
 hipError_t pick_dw(DwArgs a, hipStream_t s) {
   set_divisor(a);
+  // 256 x 128 tiles from two to a CU on: buckets of 768 rows take 37 us against
+  // 41 with 128 x 128 ones at 512 tiles (16 experts of 1024 x 1024), 51 against
+  // 53 at 768, 65 against 69 at 1024, 159 against 178 at 2048, but 24 against 21
+  // at 256 and 20 against 13 at 8. Short buckets (96 rows) differ by 5 %, and
+  // with look-ups the smaller ones are up to 18 % faster between 600 and 900.
   const int64_t pairs = static_cast<int64_t>(a.E) * ((a.N + 255) / 256) * ((a.K + 127) / 128);
   if (pairs >= 512) return launch_dw<TYPE, 256, 128>(a, s);
   return launch_dw<TYPE, 128, 128>(a, s);
