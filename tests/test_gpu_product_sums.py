@@ -106,3 +106,18 @@ def test_what_the_fp8_instruction_drops(M, N, K, kind):
     d = y[at].double() - exact
     assert abs(d.sum().item()) <= m.sum().item() + 5 * ((step ** 2 / 12 + v).sum().sqrt().item()) \
         + (2.0 ** -23 * (K + 4) * mag).sum().item()
+
+
+def test_f32_sums_on_another_stream():
+    """The call that makes a given stream current passes every argument on."""
+    a, b = torch.zeros(3, 128), torch.zeros(8, 128)
+    a[:, :3], b[:, :3] = torch.tensor([256.0, 256.0, 2.0]), torch.tensor([256.0, -256.0, 2.0])
+    a, b, sa, sb = e4m3(a).cuda(), e4m3(b).cuda(), ones(3, 128), ones(1, 128)
+    off, perm = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([0, 3], [2, 0, 1]))
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    y = qm.matmul_block(a, sa, b, sb, stream=stream, f32_sums=True)
+    z = qm.grouped_matmul_block(a, sa, b[None], sb[None], off, perm, 1, "token", "slot", stream=stream, f32_sums=True)
+    stream.synchronize()
+    for got in (y, z):
+        assert got.dtype == torch.bfloat16 and (got == 4).all()
