@@ -7,8 +7,8 @@ framework's call:
   combine_rows         rows back to tokens: the weighted sum over a token's rows
   combine_rows_grad    its gradient in the rows and in the weights
   swiglu               silu(gate) * up, and its gradient in gate and up
-  matmul_4bit          few rows times a matrix held in 4 bits with group scales (affine or MXFP4)
-  grouped_matmul_4bit  the same, rows grouped by expert
+  matmul_packed          few rows times a matrix held in 4 bits with group scales (affine or MXFP4)
+  grouped_matmul_packed  the same, rows grouped by expert
 
 Sizes follow the layer this framework computes: hidden 4096, intermediate 2048, 256 experts, top-6, 1 to 4096 tokens,
 vocabulary 129280.
@@ -50,16 +50,16 @@ def listed():
         # backward pass of the activation, 4096 tokens at top-6
         dict(name="swiglu grad 24576 rows", op="swiglu", rows=24576, inner=2048, grad=True, dtype="bf16"),
         # one token through a head over the vocabulary
-        dict(name="4-bit head 1 token", op="matmul_4bit", M=1, N=129280, K=4096, format="affine", group=64,
+        dict(name="4-bit head 1 token", op="matmul_packed", M=1, N=129280, K=4096, format="affine", group=64,
              dtype="bf16", out="f32"),
         # a few sequences decoded together through a dense projection of odd size
-        dict(name="4-bit dense 13 tokens", op="matmul_4bit", M=13, N=2053, K=4000, format="affine", group=32,
+        dict(name="4-bit dense 13 tokens", op="matmul_packed", M=13, N=2053, K=4000, format="affine", group=32,
              dtype="f16", out="f16"),
         # single-token decode: six of 256 experts, gate and up stacked
-        dict(name="4-bit experts 1 token", op="grouped_matmul_4bit", T=1, k=6, E=256, N=4096, K=4096, format="affine",
+        dict(name="4-bit experts 1 token", op="grouped_matmul_packed", T=1, k=6, E=256, N=4096, K=4096, format="affine",
              group=64, x="token", y="bucket", dtype="bf16", out="bf16", skew=0.5),
         # the down projection of a 64-token decode batch, back in slot order in fp32 for the combine
-        dict(name="4-bit experts 64 tokens", op="grouped_matmul_4bit", T=64, k=6, E=256, N=4096, K=2048, format="mxfp4",
+        dict(name="4-bit experts 64 tokens", op="grouped_matmul_packed", T=64, k=6, E=256, N=4096, K=2048, format="mxfp4",
              group=32, x="bucket", y="slot", dtype="bf16", out="f32", skew=0.5),
     ]
 
@@ -69,8 +69,8 @@ def _log_uniform(rng, lo, hi):
 
 
 def draw(rng):
-    op = rng.choice(["gather_rows", "combine_rows", "combine_rows_grad", "swiglu", "matmul_4bit",
-                     "grouped_matmul_4bit"])
+    op = rng.choice(["gather_rows", "combine_rows", "combine_rows_grad", "swiglu", "matmul_packed",
+                     "grouped_matmul_packed"])
     dtype = rng.choice(["bf16", "f16", "f32"])
     if op == "swiglu":
         c = dict(op=op, rows=_log_uniform(rng, 1, 24576), grad=rng.random() < 0.6, dtype=dtype)
@@ -96,7 +96,7 @@ def draw(rng):
     c = dict(op=op, K=128 * _log_uniform(rng, 1, 64) if rng.random() < 0.6 else group * _log_uniform(rng, 2, 8192 // group),
              format=fmt, group=group, dtype=rng.choice(["bf16", "f16"]))
     c["out"] = rng.choice([c["dtype"], "f32"])
-    if op == "matmul_4bit":
+    if op == "matmul_packed":
         c.update(M=_log_uniform(rng, 1, 64), N=_log_uniform(rng, 64, 32768))
         return c
     E = _log_uniform(rng, 8, 256)
@@ -122,10 +122,10 @@ def work(case):
     if c["op"] == "swiglu":
         n, s = c["rows"] * c["inner"], SIZE[c["dtype"]]
         return {"bytes": n * s * (5 if c["grad"] else 3), "flops": n * (12 if c["grad"] else 6)}
-    if c["op"] in ("matmul_4bit", "grouped_matmul_4bit"):
+    if c["op"] in ("matmul_packed", "grouped_matmul_packed"):
         N, K = c["N"], c["K"]
         matrix = N * K / 2 + N * (K // c["group"]) * (4 if c["format"] == "affine" else 1)
-        if c["op"] == "matmul_4bit":
+        if c["op"] == "matmul_packed":
             M, rows, used = c["M"], c["M"], 1
         else:
             M, used = c["T"] * c["k"], _experts_used(c)
@@ -205,7 +205,7 @@ def prepare(case, seed):
         s["gu"] = _activations(g, c["rows"], 2 * c["inner"], DTYPES[c["dtype"]])
         s["dh"] = (torch.randn(c["rows"], c["inner"], generator=g, device="cuda") * 0.1).to(DTYPES[c["dtype"]])
         return s
-    if c["op"] == "matmul_4bit":
+    if c["op"] == "matmul_packed":
         s["x"] = _activations(g, c["M"], c["K"], DTYPES[c["dtype"]])
         codes, scales, biases = _packed(g, 1, c["N"], c["K"], c["format"], c["group"])
         s["codes"], s["scales"], s["biases"] = codes[0], scales[0], None if biases is None else biases[0]
@@ -258,7 +258,7 @@ def run(state):
             return (gate * sig * up).to(DTYPES[c["dtype"]])
         dh = state["dh"].float()
         return torch.cat([dh * up * sig * (1 + gate * (1 - sig)), dh * gate * sig], dim=1).to(DTYPES[c["dtype"]])
-    if c["op"] == "matmul_4bit":
+    if c["op"] == "matmul_packed":
         w = _dequantize(state["codes"], state["scales"], state["biases"], c["format"], c["group"])
         return (state["x"].float() @ w.t()).to(DTYPES[c["out"]])
     k, perm, weights = c["k"], state["perm"].long(), state["weights"]
@@ -307,10 +307,10 @@ def _run_own(state):
     c = state["case"]
     if c["op"] == "swiglu":
         return qm.swiglu_grad(state["gu"], state["dh"]) if c["grad"] else qm.swiglu(state["gu"])
-    if c["op"] == "matmul_4bit":
-        return qm.matmul_4bit(state["x"], state["codes"], state["scales"], state["biases"], out_dtype=c["out"])
-    if c["op"] == "grouped_matmul_4bit":
-        return qm.grouped_matmul_4bit(state["x"], state["codes"], state["scales"], state["biases"], state["offsets"],
+    if c["op"] == "matmul_packed":
+        return qm.matmul_packed(state["x"], state["codes"], state["scales"], state["biases"], out_dtype=c["out"])
+    if c["op"] == "grouped_matmul_packed":
+        return qm.grouped_matmul_packed(state["x"], state["codes"], state["scales"], state["biases"], state["offsets"],
                                       perm=state["perm"], top_k=c["k"], x_order=c["x"], out_order=c["y"],
                                       out_dtype=c["out"])
     if c["op"] == "gather_rows":
@@ -356,7 +356,7 @@ def exact(case, seed):
             return gate * sig * up
         dh = s["dh"].double()
         return torch.cat([dh * up * (sig + gate * sig * torch.sigmoid(-gate)), dh * gate * sig], dim=1)
-    if c["op"] == "matmul_4bit":
+    if c["op"] == "matmul_packed":
         parts = []
         for r in range(0, c["N"], 16384):
             w = _exact_weights(s["codes"][r:r + 16384], s["scales"][r:r + 16384],
