@@ -3,10 +3,10 @@
 Six operators, each in a plain form (elementary torch operations in 32 bits) and, where ``own`` is true, as the
 framework's call:
 
-  gather_rows          rows of tokens brought into bucket order (expert by expert), times their weight where asked
-  combine_rows         rows back to tokens: the weighted sum over a token's rows
-  combine_rows_grad    its gradient in the rows and in the weights
-  swiglu               silu(gate) * up, and its gradient in gate and up
+  gather_rows            rows of tokens brought into bucket order (expert by expert), times their weight where asked
+  combine_rows           rows back to tokens: the weighted sum over a token's rows
+  combine_rows_grad      its gradient in the rows and in the weights
+  swiglu                 silu(gate) * up, and its gradient in gate and up
   matmul_packed          few rows times a matrix held in 4 bits with group scales (affine or MXFP4)
   grouped_matmul_packed  the same, rows grouped by expert
 
