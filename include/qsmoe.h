@@ -81,7 +81,8 @@ typedef enum { MOE_ROWS_BUCKET = 0, MOE_ROWS_TOKEN = 1, MOE_ROWS_SLOT = 2 } moe_
 #define MOE_DEVERR_QUANT_INPUT 8 /* moe_quantize_affine: a NaN/inf weight, or a group's
                                     scale or bias beyond fp16 (outputs unspecified);
                                     moe_quantize_block: a NaN/inf input */
-#define MOE_DEVERR_ROW_INDEX 16 /* a perm entry of a grouped product outside its rows */
+#define MOE_DEVERR_ROW_INDEX 16 /* a perm entry of a grouped product outside its rows;
+                                   a perm or positions entry of the row steps */
 
 /*
  * One stacked quantised projection: num_experts matrices of [rows][cols].
@@ -498,6 +499,105 @@ moe_status moe_grouped_matmul(const void* x, const void* w, int32_t dtype, int32
 moe_status moe_grouped_matmul_dw(const void* x, const void* dy, int32_t dtype, int32_t T, int32_t k, int32_t N,
                                  int32_t K, int32_t E, const int32_t* offsets, const int32_t* perm, int32_t x_order,
                                  int32_t dy_order, int32_t out_dtype, void* out, int32_t* err, hipStream_t stream);
+
+/*
+ * The steps around the experts' products, each a call of its own: rows brought
+ * into bucket order and back with the router's weights, the activation between
+ * the two products, the gradients of both, and products with 4-bit weights.
+ * Assignments, offsets and perm are those of moe_permute. Types are moe_dtype;
+ * everything is computed in fp32, sums in a fixed order, with one rounding to
+ * the output; no workspace. Outputs must not overlap inputs.
+ * Sizes: T*k and n <= 2^30, k >= 1, d and inner <= 2^20, any of them odd.
+ * Pointers are aligned to their elements (err, perm, positions and weights to
+ * 4 bytes).
+ *
+ * moe_invert_perm: the bucket position of every assignment. positions int32
+ * [size] (written): positions[perm[p]] = p for p = 0 .. n - 1, -1 where perm
+ * names no position, the last one where perm names an assignment twice. perm's
+ * entries are -1 (a position without an assignment) or in [0, size); others set
+ * MOE_DEVERR_ROW_INDEX in *err (device int32 or NULL) and count as -1.
+ *
+ * moe_gather_rows: out[p] = x[perm[p] / k] (x_order MOE_ROWS_TOKEN, x [T][d])
+ * or x[perm[p]] (MOE_ROWS_SLOT, x [T*k][d]) for p = 0 .. n - 1, times
+ * topk_w[perm[p]] if topk_w (fp32 [T*k]) is not NULL. out [n][d]. The row of an
+ * entry -1 is not written; an entry outside [-1, T*k) sets
+ * MOE_DEVERR_ROW_INDEX and its row is not written either. Without weights and
+ * with one type the rows are copied bit for bit.
+ *
+ * moe_combine_rows: out[t] = sum over j = 0 .. k - 1, in order, of topk_w[t][j]
+ * * y[positions[t * k + j]], plus y_shared[t] if not NULL. y [n][d] and
+ * y_shared [T][d] of type dtype; topk_w NULL: ones; positions NULL: y is in
+ * slot order, [T*k][d] (n == T*k). A position -1 adds nothing (y's row and its
+ * weight are not read), one outside [-1, n) sets MOE_DEVERR_ROW_INDEX and adds
+ * nothing. This is also the gradient of moe_gather_rows in x.
+ *
+ * moe_combine_rows_grad: the gradient of moe_combine_rows in y and the weights:
+ * dy[p] = topk_w[a] * dout[a / k] and dw[a] = sum over columns of dout[a / k] *
+ * y[p], p = positions[a]. dout [T][d] of type dout_dtype, dy [n][d] of y's type
+ * dtype, dw fp32 [T][k] (zero for a position -1). Rows of dy that no position
+ * names are not written; where two assignments name one row, dy holds one of
+ * their two gradients (moe_invert_perm gives no such positions). y_shared's
+ * gradient is dout.
+ * The gradient of moe_gather_rows in its weights is this call's dw with x in
+ * the place of dout and the gathered rows' gradient in the place of y.
+ *
+ * Nothing to write: MOE_OK without a launch (d == 0 still writes dw's zeros).
+ * Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, HIP.
+ */
+moe_status moe_invert_perm(const int32_t* perm, int32_t n, int32_t size, int32_t* positions, int32_t* err,
+                           hipStream_t stream);
+
+moe_status moe_gather_rows(const void* x, int32_t dtype, int32_t T, int32_t k, int32_t d, int32_t x_order,
+                           const int32_t* perm, int32_t n, const float* topk_w, int32_t out_dtype, void* out,
+                           int32_t* err, hipStream_t stream);
+
+moe_status moe_combine_rows(const void* y, int32_t dtype, int32_t n, const int32_t* positions, const float* topk_w,
+                            const void* y_shared, int32_t T, int32_t k, int32_t d, int32_t out_dtype, void* out,
+                            int32_t* err, hipStream_t stream);
+
+moe_status moe_combine_rows_grad(const void* dout, int32_t dout_dtype, const void* y, int32_t dtype, int32_t n,
+                                 const int32_t* positions, const float* topk_w, int32_t T, int32_t k, int32_t d,
+                                 void* dy, float* dw, int32_t* err, hipStream_t stream);
+
+/* moe_swiglu: h = silu(gate) * up of gu [rows][2 * inner], gate in its first
+ * `inner` columns and up in the others (as moe_swiglu_quantize_block); h
+ * [rows][inner] of gu's type. moe_swiglu_grad: its gradient, with s = 1 / (1 +
+ * e^-gate): dgu [rows][2 * inner] of gu's type holds dh * up * s * (1 + gate *
+ * (1 - s)) and dh * gate * s; dh [rows][inner] of type dh_dtype. Infinities and
+ * NaN follow these formulas (gate = -inf gives NaN). */
+moe_status moe_swiglu(const void* gu, int32_t dtype, int64_t rows, int32_t inner, void* h, hipStream_t stream);
+moe_status moe_swiglu_grad(const void* gu, int32_t dtype, const void* dh, int32_t dh_dtype, int64_t rows,
+                           int32_t inner, void* dgu, hipStream_t stream);
+
+/*
+ * moe_matmul_packed: out[m][n] = sum_k x[m][k] * W[n][k] for W held in 4 bits as
+ * a moe_qtensor holds it: MOE_FMT_AFFINE (group 32, 64 or 128; fp16 scales and
+ * biases) or MOE_FMT_MXFP4 (group 32; e8m0 scales, biases NULL). x bf16 or fp16
+ * [M][K]; codes uint32 [N][K / 8], scales and biases [N][K / group].
+ * moe_grouped_matmul_packed: the same with codes [E][N][K / 8] and so on, rows
+ * grouped by expert as in moe_grouped_matmul (positions outside every bucket,
+ * clamped offsets and perm entries out of range as described there).
+ * Meant for few rows of x for each matrix (tokens being decoded): each pass
+ * over a matrix takes 4 to 64 rows. Products are exact, sums fp32: within a
+ * group sum x * code and sum x are formed first and multiplied by the scale
+ * and added with the bias then, so a row of x with an infinity or a NaN (or one
+ * of 2^117 and more) gives values that are not finite, and so does such a
+ * scale or bias; other rows are not affected. One rounding to out_dtype.
+ * K % 32 == 0, K % group == 0, K >= 32, N any; N and K <= 2^20, M and T*k <=
+ * 2^30, E <= 1024, k >= 1. x and codes 16-byte, scales, biases and out aligned
+ * to their elements, offsets, perm and err to 4 bytes. M, T or N of 0: MOE_OK.
+ * Errors: INVALID_ARG, UNSUPPORTED (sizes, format, group, fp32 x), ALIGNMENT,
+ * HIP.
+ */
+moe_status moe_matmul_packed(const void* x, int32_t dtype, const uint32_t* codes, const void* scales,
+                           const uint16_t* biases, int32_t format, int32_t group, int32_t M, int32_t N, int32_t K,
+                           int32_t out_dtype, void* out, hipStream_t stream);
+
+moe_status moe_grouped_matmul_packed(const void* x, int32_t dtype, const uint32_t* codes, const void* scales,
+                                   const uint16_t* biases, int32_t format, int32_t group, int32_t T, int32_t k,
+                                   int32_t N, int32_t K, int32_t E, const int32_t* offsets, const int32_t* perm,
+                                   int32_t x_order, int32_t out_order, int32_t out_dtype, void* out, int32_t* err,
+                                   hipStream_t stream);
 
 const char* moe_status_string(moe_status status);
 

@@ -10,3 +10,4 @@ against the pages it cites; see ``oracle.moe``.
 """
 from .moe import *  # noqa: F401,F403
 from .products import *  # noqa: F401,F403
+from .steps import *  # noqa: F401,F403

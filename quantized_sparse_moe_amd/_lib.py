@@ -101,6 +101,16 @@ _SIGS = {
     "moe_grouped_matmul": (c_int32, [c_void_p] * 2 + [c_int32] * 6 + [c_void_p] * 2 + [c_int32] * 4 + [c_void_p] * 3),
     "moe_grouped_matmul_dw": (c_int32, [c_void_p] * 2 + [c_int32] * 6 + [c_void_p] * 2 + [c_int32] * 3
                               + [c_void_p] * 3),
+    "moe_invert_perm": (c_int32, [c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p]),
+    "moe_gather_rows": (c_int32, [c_void_p] + [c_int32] * 5 + [c_void_p, c_int32, c_void_p, c_int32] + [c_void_p] * 3),
+    "moe_combine_rows": (c_int32, [c_void_p, c_int32, c_int32] + [c_void_p] * 3 + [c_int32] * 4 + [c_void_p] * 3),
+    "moe_combine_rows_grad": (c_int32, [c_void_p, c_int32, c_void_p, c_int32, c_int32] + [c_void_p] * 2
+                              + [c_int32] * 3 + [c_void_p] * 4),
+    "moe_swiglu": (c_int32, [c_void_p, c_int32, c_int64, c_int32, c_void_p, c_void_p]),
+    "moe_swiglu_grad": (c_int32, [c_void_p, c_int32, c_void_p, c_int32, c_int64, c_int32, c_void_p, c_void_p]),
+    "moe_matmul_packed": (c_int32, [c_void_p, c_int32] + [c_void_p] * 3 + [c_int32] * 6 + [c_void_p] * 2),
+    "moe_grouped_matmul_packed": (c_int32, [c_void_p, c_int32] + [c_void_p] * 3 + [c_int32] * 7 + [c_void_p] * 2
+                                + [c_int32] * 3 + [c_void_p] * 3),
     "moe_status_string": (c_char_p, [c_int32]),
     "moe_version": (c_char_p, []),
 }

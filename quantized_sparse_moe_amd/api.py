@@ -620,3 +620,264 @@ def grouped_matmul_dw(x: torch.Tensor, dy: torch.Tensor, offsets: torch.Tensor, 
         None if perm is None else perm.data_ptr(), _lib.MOE_ROWS[x_order], _lib.MOE_ROWS.get(dy_order, -1),
         _DT[dw.dtype], dw.data_ptr(), _err_ptr(err, dev), _raw_stream(dev.index)), "moe_grouped_matmul_dw")
     return dw
+
+
+# -- rows to buckets and back, SwiGLU, 4-bit products ---------------------------
+
+_WEIGHT16 = (torch.float16, torch.int16)  # fp16 scales and biases, as such or as quantize_affine's bit patterns
+
+
+def _rows(T: int, k: int, n: int, *sizes: int) -> None:
+    if k < 1:
+        raise ValueError("top_k must be at least 1")
+    _sides(T * k, n, *sizes)
+
+
+def _weights(weights: Optional[torch.Tensor], T: int, k: int, dev) -> Optional[int]:
+    if weights is None:
+        return None
+    _shape(_operand(weights, "weights", _F32, (2,), dev), "weights", (T, k))
+    return weights.data_ptr()
+
+
+def invert_perm(perm: torch.Tensor, size: Optional[int] = None, err: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+    """The bucket position of every assignment (moe_invert_perm): positions
+    int32 [size] with positions[perm[p]] = p, -1 where perm names none; size is
+    perm's length unless given."""
+    dev = _operand(perm, "perm", _I32, (1,)).device
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return invert_perm(perm, size, err)
+    n = perm.shape[0]
+    if size is None:
+        size = n
+    if size < 0:
+        raise ValueError("size must not be negative")
+    _sides(n, size)
+    positions = torch.empty(size, dtype=torch.int32, device=dev)
+    check(_lib.load().moe_invert_perm(perm.data_ptr(), n, size, positions.data_ptr(), _err_ptr(err, dev),
+                                      _raw_stream(dev.index)), "moe_invert_perm")
+    return positions
+
+
+def gather_rows(x: torch.Tensor, perm: torch.Tensor, top_k: int = 1, x_order: str = "token",
+                weights: Optional[torch.Tensor] = None, out_dtype: Optional[str] = None,
+                out: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Rows in bucket order (moe_gather_rows): out[p] = x[perm[p] // top_k]
+    (`x_order` "token") or x[perm[p]] ("slot"), times weights[T][top_k] at
+    perm[p] if given. Rows of entries -1 are not written. The output type is x's
+    unless `out_dtype` or `out` says otherwise. Not recorded by autograd
+    (operands that require grad are refused): the gradient in x is combine_rows
+    of the rows' gradient, the one in the weights combine_rows_grad's second
+    result for (x, the rows' gradient, weights)."""
+    if x.requires_grad or (weights is not None and weights.requires_grad):
+        _unrecorded("gather_rows")
+    dev = _operand(x, "x", _DT, (2,)).device
+    if x_order not in ("token", "slot"):
+        raise ValueError(f"row order must be token or slot, got {x_order!r}")
+    rows, d = x.shape
+    n = _operand(perm, "perm", _I32, (1,), dev).shape[0]
+    T = rows if x_order == "token" else rows // max(top_k, 1)
+    _rows(T, top_k, n, d)
+    if x_order == "slot" and rows != T * top_k:
+        raise ValueError(f"{rows} rows in slot order are no multiple of top_k = {top_k}")
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return gather_rows(x, perm, top_k, x_order, weights, out_dtype, out, err)
+    w = _weights(weights, T, top_k, dev)
+    y = _out(out, (n, d), x.dtype if out_dtype is None else _out_type(out_dtype), dev)
+    check(_lib.load().moe_gather_rows(x.data_ptr(), _DT[x.dtype], T, top_k, d, _lib.MOE_ROWS[x_order],
+                                      perm.data_ptr(), n, w, _DT[y.dtype], y.data_ptr(), _err_ptr(err, dev),
+                                      _raw_stream(dev.index)), "moe_gather_rows")
+    return y
+
+
+def _slots(rows: int, positions: Optional[torch.Tensor], weights: Optional[torch.Tensor], top_k: Optional[int], dev):
+    """(T, top_k) of rows in slot order, or of rows in bucket order by their positions."""
+    if top_k is None:
+        top_k = weights.shape[1] if weights is not None and weights.dim() == 2 else 1
+    if top_k < 1:
+        raise ValueError("top_k must be at least 1")
+    slots = rows if positions is None else _operand(positions, "positions", _I32, (1,), dev).shape[0]
+    if slots % top_k:
+        raise ValueError(f"{slots} {'rows in slot order' if positions is None else 'positions'} are no multiple of "
+                         f"top_k = {top_k}")
+    return slots // top_k, top_k
+
+
+def combine_rows(y: torch.Tensor, weights: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                 top_k: Optional[int] = None, y_shared: Optional[torch.Tensor] = None,
+                 out_dtype: Optional[str] = None, out: Optional[torch.Tensor] = None,
+                 err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The weighted sum over each token's rows, and y_shared (moe_combine_rows):
+    y [rows][d] in slot order, or in bucket order with `positions` from
+    invert_perm (-1: no row); weights fp32 [T][top_k], None for ones (then
+    `top_k` tells the slots of a token) -> [T][d] of y's type unless `out_dtype`
+    or `out` says otherwise. `combine` is the same for fp32 rows in slot order.
+    Not recorded by autograd (operands that require grad are refused): the
+    gradients are combine_rows_grad's."""
+    if y.requires_grad or (weights is not None and weights.requires_grad) or (
+            y_shared is not None and y_shared.requires_grad):
+        _unrecorded("combine_rows")
+    dev = _operand(y, "y", _DT, (2,)).device
+    n, d = y.shape
+    T, top_k = _slots(n, positions, weights, top_k, dev)
+    _rows(T, top_k, n, d)
+    if y_shared is not None:
+        _shape(_operand(y_shared, "y_shared", (y.dtype,), (2,), dev), "y_shared", (T, d))
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return combine_rows(y, weights, positions, top_k, y_shared, out_dtype, out, err)
+    w = _weights(weights, T, top_k, dev)
+    o = _out(out, (T, d), y.dtype if out_dtype is None else _out_type(out_dtype), dev)
+    check(_lib.load().moe_combine_rows(y.data_ptr(), _DT[y.dtype], n, None if positions is None else positions.data_ptr(),
+                                       w, None if y_shared is None else y_shared.data_ptr(), T, top_k, d, _DT[o.dtype],
+                                       o.data_ptr(), _err_ptr(err, dev), _raw_stream(dev.index)), "moe_combine_rows")
+    return o
+
+
+def combine_rows_grad(dout: torch.Tensor, y: torch.Tensor, weights: torch.Tensor,
+                      positions: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                      err: Optional[torch.Tensor] = None, stream=None):
+    """The gradients of combine_rows (moe_combine_rows_grad): dout [T][d], y and
+    weights as there -> (dy of y's shape and type, dweights fp32 [T][top_k]).
+    Rows of dy that no position names are not written. `out` takes dy."""
+    if dout.requires_grad or y.requires_grad or weights.requires_grad:
+        _unrecorded("combine_rows_grad")
+    dev = _operand(dout, "dout", _DT, (2,)).device
+    n, d = _operand(y, "y", _DT, (2,), dev).shape
+    T, top_k = _slots(n, positions, _operand(weights, "weights", _F32, (2,), dev), None, dev)
+    _rows(T, top_k, n, d)
+    _shape(dout, "dout", (T, d))
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return combine_rows_grad(dout, y, weights, positions, out, err)
+    w = _weights(weights, T, top_k, dev)
+    dy = _out(out, (n, d), y.dtype, dev)
+    if dy.dtype != y.dtype:
+        raise TypeError(f"out must be {y.dtype} as y, got {dy.dtype}")
+    dw = torch.empty(T, top_k, dtype=torch.float32, device=dev)
+    check(_lib.load().moe_combine_rows_grad(
+        dout.data_ptr(), _DT[dout.dtype], y.data_ptr(), _DT[y.dtype], n,
+        None if positions is None else positions.data_ptr(), w, T, top_k, d, dy.data_ptr(), dw.data_ptr(),
+        _err_ptr(err, dev), _raw_stream(dev.index)), "moe_combine_rows_grad")
+    return dy, dw
+
+
+def swiglu(gu: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """silu(gate) * up of gu [rows][gate | up] (moe_swiglu) -> [rows][inner] of
+    gu's type. Not recorded by autograd (a gu that requires grad is refused): the
+    gradient is swiglu_grad."""
+    if gu.requires_grad:
+        _unrecorded("swiglu")
+    dev = _operand(gu, "gu", _DT, (2,)).device
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return swiglu(gu, out)
+    rows, two = gu.shape
+    if two % 2:
+        raise ValueError("gu must hold gate and up columns in equal number")
+    _sides(two)
+    h = _out(out, (rows, two // 2), gu.dtype, dev)
+    if h.dtype != gu.dtype:
+        raise TypeError(f"out must be {gu.dtype} as gu, got {h.dtype}")
+    check(_lib.load().moe_swiglu(gu.data_ptr(), _DT[gu.dtype], rows, two // 2, h.data_ptr(), _raw_stream(dev.index)),
+          "moe_swiglu")
+    return h
+
+
+def swiglu_grad(gu: torch.Tensor, dh: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The gradient of swiglu (moe_swiglu_grad): gu [rows][gate | up], dh
+    [rows][inner] -> dgu of gu's shape and type."""
+    if gu.requires_grad or dh.requires_grad:
+        _unrecorded("swiglu_grad")
+    dev = _operand(gu, "gu", _DT, (2,)).device
+    rows, two = gu.shape
+    if two % 2:
+        raise ValueError("gu must hold gate and up columns in equal number")
+    _sides(two)
+    _shape(_operand(dh, "dh", _DT, (2,), dev), "dh", (rows, two // 2))
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return swiglu_grad(gu, dh, out)
+    dgu = _out(out, (rows, two), gu.dtype, dev)
+    if dgu.dtype != gu.dtype:
+        raise TypeError(f"out must be {gu.dtype} as gu, got {dgu.dtype}")
+    check(_lib.load().moe_swiglu_grad(gu.data_ptr(), _DT[gu.dtype], dh.data_ptr(), _DT[dh.dtype], rows, two // 2,
+                                      dgu.data_ptr(), _raw_stream(dev.index)), "moe_swiglu_grad")
+    return dgu
+
+
+def _packed(codes: torch.Tensor, scales: torch.Tensor, biases: Optional[torch.Tensor], lead: tuple, K: int, dev):
+    """(format, group, biases' address) of 4-bit weights [*lead][K], after checks of their three parts."""
+    dims = (len(lead) + 1,)
+    if K % 32 or K == 0:
+        raise ValueError(f"the contraction must be a positive multiple of 32, got {K}")
+    _shape(_operand(codes, "codes", _I32, dims, dev), "codes", (*lead, K // 8))
+    _operand(scales, "scales", (torch.uint8,) if biases is None else _WEIGHT16, dims, dev)
+    groups = scales.shape[-1]
+    if groups == 0 or K % groups:
+        raise ValueError(f"{groups} groups do not divide {K} columns")
+    _shape(scales, "scales", (*lead, groups))
+    if biases is None:
+        return _lib.MOE_FMT_MXFP4, K // groups, None
+    _shape(_operand(biases, "biases", _WEIGHT16, dims, dev), "biases", (*lead, groups))
+    return _lib.MOE_FMT_AFFINE, K // groups, biases.data_ptr()
+
+
+def _grad_of_packed(x, scales, biases) -> bool:
+    return x.requires_grad or scales.requires_grad or (biases is not None and biases.requires_grad)
+
+
+def matmul_packed(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, biases: Optional[torch.Tensor] = None,
+                out_dtype: Optional[str] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """x [M][K] (bf16 or fp16) times W^T of 4-bit weights (moe_matmul_packed): codes
+    int32 [N][K / 8] with scales and biases [N][K / group] as quantize_affine
+    gives them (fp16, or their int16 bit patterns), or MXFP4 with uint8 scales
+    [N][K / 32] and no biases -> [M][N] of x's type unless `out_dtype` or `out`
+    says otherwise. For few rows. Not recorded by autograd: operands that require
+    grad are refused."""
+    if _grad_of_packed(x, scales, biases):
+        _unrecorded("matmul_packed")
+    dev = _operand(x, "x", _B16, (2,)).device
+    M, K = x.shape
+    N = _operand(codes, "codes", _I32, (2,), dev).shape[0]
+    _sides(M, N, K)
+    fmt, group, b = _packed(codes, scales, biases, (N,), K, dev)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return matmul_packed(x, codes, scales, biases, out_dtype, out)
+    y = _out(out, (M, N), x.dtype if out_dtype is None else _out_type(out_dtype), dev)
+    check(_lib.load().moe_matmul_packed(x.data_ptr(), _DT[x.dtype], codes.data_ptr(), scales.data_ptr(), b, fmt, group,
+                                      M, N, K, _DT[y.dtype], y.data_ptr(), _raw_stream(dev.index)), "moe_matmul_packed")
+    return y
+
+
+def grouped_matmul_packed(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, biases: Optional[torch.Tensor],
+                        offsets: torch.Tensor, perm: Optional[torch.Tensor] = None, top_k: int = 1,
+                        x_order: str = "bucket", out_order: str = "bucket", out_dtype: Optional[str] = None,
+                        out: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None,
+                        stream=None) -> torch.Tensor:
+    """Rows grouped by expert times their expert's 4-bit weights
+    (moe_grouped_matmul_packed): codes int32 [E][N][K / 8], scales and biases as in
+    matmul_packed with E in front, orders, offsets and perm as in grouped_matmul ->
+    [T * top_k][N] in `out_order`. Rows of no bucket are not written."""
+    if _grad_of_packed(x, scales, biases):
+        _unrecorded("grouped_matmul_packed")
+    dev = _operand(x, "x", _B16, (2,)).device
+    rows, K = x.shape
+    E, N, _ = _operand(codes, "codes", _I32, (3,), dev).shape
+    T = _groups(rows, x_order, top_k, offsets, perm, E, N, K, dev)
+    fmt, group, b = _packed(codes, scales, biases, (E, N), K, dev)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return grouped_matmul_packed(x, codes, scales, biases, offsets, perm, top_k, x_order, out_order, out_dtype,
+                                       out, err)
+    y = _out(out, (T * top_k, N), x.dtype if out_dtype is None else _out_type(out_dtype), dev)
+    check(_lib.load().moe_grouped_matmul_packed(
+        x.data_ptr(), _DT[x.dtype], codes.data_ptr(), scales.data_ptr(), b, fmt, group, T, top_k, N, K, E,
+        offsets.data_ptr(), None if perm is None else perm.data_ptr(), _lib.MOE_ROWS[x_order],
+        _lib.MOE_ROWS.get(out_order, -1), _DT[y.dtype], y.data_ptr(), _err_ptr(err, dev), _raw_stream(dev.index)),
+        "moe_grouped_matmul_packed")
+    return y

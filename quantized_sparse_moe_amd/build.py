@@ -20,7 +20,8 @@ LIB = os.path.join(PKG, "libqsmoe.so")
 ARCH = "gfx950"
 
 SOURCES = ["host.hip", "router.hip", "permute.hip", "ffn_gemv.hip", "ffn_mfma.hip", "decode.hip", "combine.hip",
-           "quantize.hip", "sinkhorn.hip", "probe.hip", "host_products.hip", "quantize_block.hip", "product_tiles.hip"]
+           "quantize.hip", "sinkhorn.hip", "probe.hip", "host_products.hip", "quantize_block.hip", "product_tiles.hip",
+           "host_steps.hip", "rows.hip", "swiglu.hip", "product_packed.hip"]
 
 HIPCC_FLAGS = [
     "-O3", "-std=c++17", f"--offload-arch={ARCH}", "-fPIC", "-Wall", "-Wno-unused-function",

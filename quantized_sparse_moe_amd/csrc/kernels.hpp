@@ -186,6 +186,63 @@ struct DwArgs {
 };
 hipError_t launch_product_dw(const DwArgs& a, hipStream_t s);
 
+// Rows of tokens to buckets and back ---------------------------------------------
+hipError_t launch_invert_perm(const int32_t* perm, int n, int size, int32_t* positions, int32_t* err, hipStream_t s);
+
+struct GatherArgs {
+  const void* x;           // [T][d], or [T*k][d] in slot order
+  const int32_t* perm;     // [n]
+  const float* w;          // [T*k] or null
+  void* out;               // [n][d]
+  int32_t* err;
+  int32_t dtype, out_dtype, T, k, n, d, slot_order;
+};
+hipError_t launch_gather_rows(const GatherArgs& a, hipStream_t s);
+
+struct CombineArgs {
+  const void* y;             // [n][d]
+  const float* w;            // [T*k] or null (ones)
+  const int32_t* positions;  // [T*k] or null (slot order)
+  const void* shared;        // [T][d] or null
+  void* out;                 // [T][d]
+  int32_t* err;
+  int32_t dtype, out_dtype, T, k, n, d;
+};
+hipError_t launch_combine_rows(const CombineArgs& a, hipStream_t s);
+
+struct CombineGradArgs {
+  const void* dout;          // [T][d]
+  const void* y;             // [n][d]
+  const float* w;            // [T*k]
+  const int32_t* positions;  // [T*k] or null (slot order)
+  void* dy;                  // [n][d], y's type
+  float* dw;                 // [T*k]
+  int32_t* err;
+  int32_t dtype, dout_dtype, T, k, n, d;
+};
+hipError_t launch_combine_rows_grad(const CombineGradArgs& a, hipStream_t s);
+
+// SwiGLU of rows of gate | up, and its gradient ------------------------------------
+hipError_t launch_swiglu(const void* gu, int dtype, int64_t rows, int inner, void* h, hipStream_t s);
+hipError_t launch_swiglu_grad(const void* gu, int dtype, const void* dh, int dh_dtype, int64_t rows, int inner,
+                              void* dgu, hipStream_t s);
+
+// Products of few rows with 4-bit weights -------------------------------------------
+struct PackedArgs {
+  const void* x;           // rows in x_order, K columns
+  const uint32_t* codes;   // [E][N][K / 8]
+  const void* scales;      // fp16 (affine) or e8m0 [E][N][K / group]
+  const uint16_t* biases;  // fp16 [E][N][K / group] or null (MXFP4)
+  int32_t dtype, out_dtype;
+  int32_t T, k, E, N, K, group;
+  const int32_t* offsets;  // null: one matrix for all rows
+  const int32_t* perm;
+  int32_t x_order, out_order;
+  void* out;
+  int32_t* err;
+};
+hipError_t launch_product_packed(const PackedArgs& a, hipStream_t s);
+
 // Measurement kernels -----------------------------------------------------------
 // mode 0: read every byte of buf once (16 bytes per lane); 1: read the first
 // 32 bytes of every 128-byte line; 2: write every byte once.
