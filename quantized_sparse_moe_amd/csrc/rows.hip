@@ -22,27 +22,35 @@ namespace {
 // positions[perm[p]] = p, -1 where perm names no position. Each workgroup owns
 // kOwned assignments in LDS and reads all of perm: one launch, no atomics on
 // memory. An assignment named twice gets its last position.
-constexpr int kOwned = 1024;
+constexpr int kOwned = 1024, kAtOnce = 6;
 
 __global__ __launch_bounds__(1024) void k_invert_owned(const int32_t* __restrict__ perm, int n, int size,
                                                        int32_t* __restrict__ positions, int32_t* err) {
   __shared__ int32_t owned[kOwned];
-  const int first = blockIdx.x * kOwned;
+  const uint32_t first = blockIdx.x * kOwned, here = min(kOwned, size - static_cast<int>(first));
   owned[threadIdx.x] = -1;
   __syncthreads();
-  for (int p0 = threadIdx.x; p0 < n; p0 += 8 * 1024) {
-    int a[8];
+  for (int p0 = 4 * threadIdx.x; p0 < n; p0 += 4 * kAtOnce * 1024) {
+    Raw<kF32, 4> r[kAtOnce];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = p0 + 1024 * i < n ? perm[p0 + 1024 * i] : -1;
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int p = p0 + 4096 * i;
+      if (p < n) r[i] = load_raw<kF32, 4>(reinterpret_cast<const char*>(perm + p), n - p);
+      else r[i] = {};
+    }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int at = a[i] - first;
-      if (at >= 0 && at < kOwned && a[i] < size) atomicMax(&owned[at], p0 + 1024 * i);
-      if (blockIdx.x == 0 && (a[i] < -1 || a[i] >= size)) set_device_error(err, 16);
+    for (int i = 0; i < kAtOnce; ++i) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int p = p0 + 4096 * i + j;
+        const uint32_t a = r[i].w[j];
+        if (a - first < here && p < n) atomicMax(&owned[a - first], p);
+        if (blockIdx.x == 0 && a + 1 > static_cast<uint32_t>(size) && p < n) set_device_error(err, 16);
+      }
     }
   }
   __syncthreads();
-  if (first + static_cast<int>(threadIdx.x) < size) positions[first + threadIdx.x] = owned[threadIdx.x];
+  if (threadIdx.x < here) positions[first + threadIdx.x] = owned[threadIdx.x];
 }
 
 // Of longer lists every workgroup would read too much: the same in two
@@ -61,36 +69,52 @@ __global__ __launch_bounds__(256) void k_invert_scatter(const int32_t* __restric
   }
 }
 
-// One eight of a row per lane.
+// Row p of the result for a lane's V elements. ONCE: see store_raw.
+template <int IN, int OUT, int V, bool WEIGHTED, bool ONCE>
+__device__ __forceinline__ void gather_one(const GatherArgs& g, int64_t p, int at) {
+  const int a = g.perm[p];
+  if (a < 0 || a >= g.T * g.k) {
+    if (a != -1) set_device_error(g.err, 16);
+    return;
+  }
+  const int64_t row = g.slot_order ? a : a / g.k;
+  const auto r = load_raw<IN, V>(static_cast<const char*>(g.x) + (row * g.d + at) * kElemBytes<IN>, g.d - at);
+  char* to = static_cast<char*>(g.out) + (p * g.d + at) * kElemBytes<OUT>;
+  if constexpr (IN == OUT && !WEIGHTED) {
+    store_raw<OUT, V, ONCE>(to, r, g.d - at);
+  } else {
+    float v[V];
+    to_f32<IN, V>(r, v);
+    if constexpr (WEIGHTED) {
+      const float w = g.w[a];
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] *= w;
+    }
+    store_raw<OUT, V, ONCE>(to, from_f32<OUT, V>(v), g.d - at);
+  }
+}
+
 template <int IN, int OUT, bool WEIGHTED>
 __global__ __launch_bounds__(256) void k_gather(const GatherArgs g, const RowSplit split) {
-  const int assignments = g.T * g.k;
+  constexpr int V = kLaneElems<IN, OUT>;
   for (int64_t b = blockIdx.x; b < split.blocks; b += gridDim.x) {
     int64_t p;
     int at;
-    place_of(split, b, &p, &at);
-    if (p >= g.n || at >= g.d) continue;
-    const int a = g.perm[p];
-    if (a < 0 || a >= assignments) {
-      if (a != -1) set_device_error(g.err, 16);
-      continue;
-    }
-    const int64_t row = g.slot_order ? a : a / g.k;
-    const Raw8<IN> r = load_raw<IN>(static_cast<const char*>(g.x) + (row * g.d + at) * kElemBytes<IN>, g.d - at);
-    char* to = static_cast<char*>(g.out) + (p * g.d + at) * kElemBytes<OUT>;
-    if constexpr (IN == OUT && !WEIGHTED) {
-      store_raw<OUT>(to, r, g.d - at);
-    } else {
-      float v[8];
-      to_f32<IN>(r, v);
-      if constexpr (WEIGHTED) {
-        const float w = g.w[a];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= w;
-      }
-      store_raw<OUT>(to, from_f32<OUT>(v), g.d - at);
-    }
+    place_of<V>(split, b, &p, &at);
+    if (p < g.n && at < g.d) gather_one<IN, OUT, V, WEIGHTED, false>(g, p, at);
   }
+}
+
+// Workgroup b runs on XCD b % 8. Slices of `width` lanes' columns: each XCD
+// takes its slices one after the other, all rows of a slice together.
+template <int IN, int OUT, bool WEIGHTED>
+__global__ __launch_bounds__(256) void k_gather_slices(const GatherArgs g, const int shift, const int slices,
+                                                       const int per_slice) {
+  constexpr int V = kLaneElems<IN, OUT>;
+  const int b = blockIdx.x >> 3, slice = (blockIdx.x & 7) + 8 * (b / per_slice);
+  const int64_t p = static_cast<int64_t>(b % per_slice) * (256 >> shift) + (threadIdx.x >> shift);
+  const int at = V * ((slice << shift) + (threadIdx.x & ((1 << shift) - 1)));
+  if (slice < slices && p < g.n && at < g.d) gather_one<IN, OUT, V, WEIGHTED, true>(g, p, at);
 }
 
 // The row of assignment a, -1 for none.
@@ -102,20 +126,21 @@ __device__ __forceinline__ int row_at(const int32_t* positions, int a, int n, in
   return -1;
 }
 
-// One eight of a token per lane; the rows of kAhead slots are loaded together.
-constexpr int kAhead = 4;
+// V elements of a token per lane; the rows of kAhead slots are loaded together.
+constexpr int kAhead = 8;
 
 template <int IN, int OUT>
 __global__ __launch_bounds__(256) void k_combine_rows(const CombineArgs g, const RowSplit split) {
+  constexpr int V = kLaneElems<IN, OUT>;
   for (int64_t b = blockIdx.x; b < split.blocks; b += gridDim.x) {
     int64_t t;
     int at;
-    place_of(split, b, &t, &at);
+    place_of<V>(split, b, &t, &at);
     if (t >= g.T || at >= g.d) continue;
     const int left = g.d - at;
-    float acc[8] = {};
+    float acc[V] = {};
     for (int j0 = 0; j0 < g.k; j0 += kAhead) {
-      Raw8<IN> r[kAhead];
+      Raw<IN, V> r[kAhead];
       float w[kAhead];
       bool there[kAhead];
 #pragma unroll
@@ -126,60 +151,80 @@ __global__ __launch_bounds__(256) void k_combine_rows(const CombineArgs g, const
         w[i] = 1.0f;
         if (there[i]) {
           if (g.w) w[i] = g.w[a];
-          r[i] = load_raw<IN>(static_cast<const char*>(g.y) + (static_cast<int64_t>(p) * g.d + at) * kElemBytes<IN>, left);
+          r[i] = load_raw<IN, V>(static_cast<const char*>(g.y) + (static_cast<int64_t>(p) * g.d + at) * kElemBytes<IN>, left);
         }
       }
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         if (there[i]) {
-          float v[8];
-          to_f32<IN>(r[i], v);
+          float v[V];
+          to_f32<IN, V>(r[i], v);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) acc[e] = fmaf(w[i], v[e], acc[e]);
+          for (int e = 0; e < V; ++e) acc[e] = fmaf(w[i], v[e], acc[e]);
         }
       }
     }
     if (g.shared) {
-      float v[8];
-      to_f32<IN>(load_raw<IN>(static_cast<const char*>(g.shared) + (t * g.d + at) * kElemBytes<IN>, left), v);
+      float v[V];
+      to_f32<IN, V>(load_raw<IN, V>(static_cast<const char*>(g.shared) + (t * g.d + at) * kElemBytes<IN>, left), v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += v[e];
+      for (int e = 0; e < V; ++e) acc[e] += v[e];
     }
-    store_raw<OUT>(static_cast<char*>(g.out) + (t * g.d + at) * kElemBytes<OUT>, from_f32<OUT>(acc), left);
+    store_raw<OUT, V>(static_cast<char*>(g.out) + (t * g.d + at) * kElemBytes<OUT>, from_f32<OUT, V>(acc), left);
   }
 }
 
-// One workgroup per assignment.
+// dy's elements of one lane of 2^shift that step over a row, and the lane's part
+// of the inner product.
 template <int IN, int DOUT>
-__global__ __launch_bounds__(256) void k_combine_grad(const CombineGradArgs g) {
-  __shared__ float part[4];
-  const int assignments = g.T * g.k;
-  for (int64_t a = blockIdx.x; a < assignments; a += gridDim.x) {
-    const int p = row_at(g.positions, static_cast<int>(a), g.n, threadIdx.x == 0 ? g.err : nullptr);
-    float dot = 0.0f;
-    if (p >= 0) {
-      const float w = g.w[a];
-      const char* dout = static_cast<const char*>(g.dout) + (a / g.k) * g.d * kElemBytes<DOUT>;
-      const char* y = static_cast<const char*>(g.y) + static_cast<int64_t>(p) * g.d * kElemBytes<IN>;
-      char* dy = static_cast<char*>(g.dy) + static_cast<int64_t>(p) * g.d * kElemBytes<IN>;
-      for (int at = 8 * threadIdx.x; at < g.d; at += 8 * 256) {
-        float u[8], v[8];
-        to_f32<DOUT>(load_raw<DOUT>(dout + static_cast<int64_t>(at) * kElemBytes<DOUT>, g.d - at), u);
-        to_f32<IN>(load_raw<IN>(y + static_cast<int64_t>(at) * kElemBytes<IN>, g.d - at), v);
+__device__ __forceinline__ float combine_grad_row(const CombineGradArgs& g, int64_t a, int p, int lane, int lanes) {
+  constexpr int V = kLaneElems<IN, DOUT>;
+  const float w = g.w[a];
+  const char* dout = static_cast<const char*>(g.dout) + (a / g.k) * g.d * kElemBytes<DOUT>;
+  const char* y = static_cast<const char*>(g.y) + static_cast<int64_t>(p) * g.d * kElemBytes<IN>;
+  char* dy = static_cast<char*>(g.dy) + static_cast<int64_t>(p) * g.d * kElemBytes<IN>;
+  float dot = 0.0f;
+#pragma unroll 2
+  for (int at = V * lane; at < g.d; at += V * lanes) {
+    float u[V], v[V];
+    to_f32<DOUT, V>(load_raw<DOUT, V>(dout + at * kElemBytes<DOUT>, g.d - at), u);
+    to_f32<IN, V>(load_raw<IN, V>(y + at * kElemBytes<IN>, g.d - at), v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          dot = fmaf(u[e], v[e], dot);
-          u[e] *= w;
-        }
-        store_raw<IN>(dy + static_cast<int64_t>(at) * kElemBytes<IN>, from_f32<IN>(u), g.d - at);
-      }
+    for (int e = 0; e < V; ++e) {
+      dot = fmaf(u[e], v[e], dot);
+      u[e] *= w;
     }
-    dot = wave_sum(dot);
-    if (lane_id() == 0) part[threadIdx.x / 64] = dot;
-    __syncthreads();
-    if (threadIdx.x == 0) g.dw[a] = (part[0] + part[1]) + (part[2] + part[3]);
-    __syncthreads();
+    store_raw<IN, V>(dy + at * kElemBytes<IN>, from_f32<IN, V>(u), g.d - at);
   }
+  return dot;
+}
+
+// 2^shift lanes of a wave per assignment.
+template <int IN, int DOUT>
+__global__ __launch_bounds__(256) void k_combine_grad(const CombineGradArgs g, const int shift, const int64_t blocks) {
+  const int lane = threadIdx.x & ((1 << shift) - 1);
+  for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
+    const int64_t a = b * (256 >> shift) + (threadIdx.x >> shift);
+    const bool there = a < static_cast<int64_t>(g.T) * g.k;
+    const int p = there ? row_at(g.positions, static_cast<int>(a), g.n, g.err) : -1;
+    float dot = 0.0f;
+    if (p >= 0) dot = combine_grad_row<IN, DOUT>(g, a, p, lane, 1 << shift);
+    for (int o = 1; o < 1 << shift; o <<= 1) dot += __shfl_xor(dot, o);
+    if (there && lane == 0) g.dw[a] = dot;
+  }
+}
+
+// A workgroup per assignment, where there are few.
+template <int IN, int DOUT>
+__global__ __launch_bounds__(256) void k_combine_grad_few(const CombineGradArgs g) {
+  __shared__ float part[4];
+  const int a = blockIdx.x, p = row_at(g.positions, a, g.n, g.err);
+  float dot = 0.0f;
+  if (p >= 0) dot = combine_grad_row<IN, DOUT>(g, a, p, threadIdx.x, 256);
+  dot = wave_sum(dot);
+  if (lane_id() == 0) part[threadIdx.x / 64] = dot;
+  __syncthreads();
+  if (threadIdx.x == 0) g.dw[a] = (part[0] + part[1]) + (part[2] + part[3]);
 }
 
 }  // namespace
@@ -197,10 +242,22 @@ hipError_t launch_invert_perm(const int32_t* perm, int n, int size, int32_t* pos
 }
 
 hipError_t launch_gather_rows(const GatherArgs& g, hipStream_t s) {
-  const RowSplit split = split_rows(g.n, g.d);
   return with_type(g.dtype, [&](auto in) {
     return with_type(g.out_dtype, [&](auto out) {
-      constexpr int IN = decltype(in)::value, OUT = decltype(out)::value;
+      constexpr int IN = decltype(in)::value, OUT = decltype(out)::value, V = kLaneElems<IN, OUT>;
+      const int64_t out_bytes = static_cast<int64_t>(g.n) * g.d * kElemBytes<OUT>;
+      constexpr int shift = 5;
+      const int slices = (g.d + (V << shift) - 1) / (V << shift);
+      if (out_bytes > (int64_t{32} << 20) && slices >= 8 && slices < 1024 && g.n < (1 << 20)) {
+        const int per_slice = (g.n + (256 >> shift) - 1) / (256 >> shift);
+        const dim3 grid(static_cast<unsigned>((slices + 7) / 8 * 8 * per_slice));
+        if (g.w)
+          QSMOE_LAUNCH((k_gather_slices<IN, OUT, true>), grid, dim3(256), 0, s, g, shift, slices, per_slice);
+        else
+          QSMOE_LAUNCH((k_gather_slices<IN, OUT, false>), grid, dim3(256), 0, s, g, shift, slices, per_slice);
+        return hipGetLastError();
+      }
+      const RowSplit split = split_rows(g.n, g.d, V);
       if (g.w)
         QSMOE_LAUNCH((k_gather<IN, OUT, true>), dim3(grid_of(split.blocks)), dim3(256), 0, s, g, split);
       else
@@ -211,21 +268,29 @@ hipError_t launch_gather_rows(const GatherArgs& g, hipStream_t s) {
 }
 
 hipError_t launch_combine_rows(const CombineArgs& g, hipStream_t s) {
-  const RowSplit split = split_rows(g.T, g.d);
   return with_type(g.dtype, [&](auto in) {
     return with_type(g.out_dtype, [&](auto out) {
-      QSMOE_LAUNCH((k_combine_rows<decltype(in)::value, decltype(out)::value>), dim3(grid_of(split.blocks)), dim3(256),
-                   0, s, g, split);
+      constexpr int IN = decltype(in)::value, OUT = decltype(out)::value;
+      const RowSplit split = split_rows(g.T, g.d, kLaneElems<IN, OUT>);
+      QSMOE_LAUNCH((k_combine_rows<IN, OUT>), dim3(grid_of(split.blocks)), dim3(256), 0, s, g, split);
       return hipGetLastError();
     });
   });
 }
 
 hipError_t launch_combine_rows_grad(const CombineGradArgs& g, hipStream_t s) {
+  const int assignments = g.T * g.k;
   return with_type(g.dtype, [&](auto in) {
     return with_type(g.dout_dtype, [&](auto dout) {
-      QSMOE_LAUNCH((k_combine_grad<decltype(in)::value, decltype(dout)::value>),
-                   dim3(grid_of(static_cast<int64_t>(g.T) * g.k)), dim3(256), 0, s, g);
+      constexpr int IN = decltype(in)::value, DOUT = decltype(dout)::value, V = kLaneElems<IN, DOUT>;
+      if (g.d > 64 * V && assignments <= 1024) {
+        QSMOE_LAUNCH((k_combine_grad_few<IN, DOUT>), dim3(assignments), dim3(256), 0, s, g);
+      } else {
+        int shift = 0;
+        while (shift < 6 && (V << shift) < g.d) ++shift;
+        const int64_t blocks = (assignments + int64_t{255 >> shift}) / (256 >> shift);
+        QSMOE_LAUNCH((k_combine_grad<IN, DOUT>), dim3(grid_of(blocks)), dim3(256), 0, s, g, shift, blocks);
+      }
       return hipGetLastError();
     });
   });
