@@ -242,8 +242,8 @@ struct FewShape {
 // tokens' top-6 of 256 experts of 4096 x 4096 324 us, 5.3 TB/s of the experts
 // used. Loads that bypass the caches are 2 to 6 % slower. A third wave to a SIMD
 // is worth the registers that it costs.
-// WHOLE: a row's values are a multiple of 16 bytes, so that none of the pieces
-// ends behind its row.
+// WHOLE: a row's values and the steps at which a wave's blocks of them begin are
+// multiples of 16 bytes, so that none of the pieces ends behind its row.
 template <int TYPE, int FMT, int NG, int VR, bool WHOLE>
 __global__ __launch_bounds__(64 * kMostWaves) __attribute__((amdgpu_waves_per_eu(3))) void k_few_rows(const PackedArgs a, const FewShape f) {
   using Values = Groups<FMT, NG>;
@@ -877,7 +877,9 @@ hipError_t launch_few(const PackedArgs& a, hipStream_t s) {
                  FewShape{kw_log2, seg, own});
     return hipGetLastError();
   };
-  if (a.K / a.group * (FMT == 0 ? 2 : 1) % 16 == 0) return launch(k_few_rows<TYPE, FMT, NG, VR, true>);
+  // pieces start at multiples of 16 bytes too: of the steps of 8 bytes at even ones
+  const bool even = Groups<FMT, NG>::kStepBytes >= 16 || own % 2 == 0 || (kw == 1 && seg >= steps);
+  if (a.K / a.group * Groups<FMT, NG>::kSize % 16 == 0 && even) return launch(k_few_rows<TYPE, FMT, NG, VR, true>);
   return launch(k_few_rows<TYPE, FMT, NG, VR, false>);
 }
 

@@ -142,6 +142,78 @@ def test_grouped(shape, orders):
         close(y, want, tolerance(mag, K, group), out)
 
 
+def sampled(N):
+    """Rows of a matrix of N: the first, the last and some between."""
+    rng = np.random.default_rng(N)
+    return np.unique(np.r_[np.arange(min(N, 20)), np.arange(max(N - 35, 0), N), rng.integers(0, N, 60)])
+
+
+LARGE = [  # M, N, K (a multiple of every group, or of the smaller ones): more than 512 tiles of 16 rows
+    (1, 8209, 4096), (1, 20000, 640), (1, 8209, 160), (2, 8300, 2208), (4, 8209, 1088), (5, 8209, 2976), (8, 9001, 8192),
+    (9, 8209, 544), (16, 8209, 8192), (16, 8400, 3104), (13, 8209, 128), (17, 12500, 672), (20, 50000, 256), (33, 13000, 1184),
+    (40, 3000, 2080), (64, 49200, 160), (65, 12400, 320), (150, 5000, 544),
+]
+
+
+@pytest.mark.parametrize("fmt,group", FORMATS)
+@pytest.mark.parametrize("M,N,K", LARGE)
+def test_large_matrices(fmt, group, M, N, K):
+    """Whole waves of tiles, contractions that end inside a step, a block of scales or a segment of x; sampled rows of
+    the matrix against the oracle, and every result finite and written."""
+    K -= K % group
+    rng = np.random.default_rng(M + N + K)
+    dtype, out = (("bf16", "f32"), ("f16", "f16"))[rng.integers(2)]
+    x = torch.from_numpy(rng.standard_normal((M, K))).to(DT[dtype])
+    codes, s, b = weights(rng, (N,), K, fmt, group)
+    y = qm.matmul_packed(x.cuda(), *on_device((codes, s, b)), out=torch.full((M, N), float("nan"), dtype=DT[out], device="cuda"))
+    assert torch.isfinite(y).all()
+    at = sampled(N)
+    want, mag = oracle.matmul_packed(x.double().numpy(), codes[at], s[at], None if b is None else b[at])
+    close(y[:, torch.from_numpy(at).cuda()], want, tolerance(mag, K, group), out)
+
+
+MANY_BUCKETS = [  # T, k, E, N, K, skew: few rows a bucket over many tiles, long buckets among them, tiles of rows
+    (3, 2, 300, 1500, 160, 0.0), (40, 4, 64, 160, 608, 1.5), (30, 8, 40, 300, 1120, 2.5), (100, 4, 256, 16, 352, 0.0),
+    (60, 5, 100, 80, 736, 0.3), (64, 6, 32, 300, 2048, 0.5), (300, 4, 40, 272, 416, 1.0), (512, 2, 8, 130, 288, 0.5),
+    (200, 3, 1000, 50, 192, 0.1),
+]
+
+
+@pytest.mark.parametrize("fmt,group", FORMATS)
+@pytest.mark.parametrize("T,k,E,N,K,skew", MANY_BUCKETS)
+def test_many_buckets(fmt, group, T, k, E, N, K, skew):
+    K -= K % group
+    rng, off, perm, _ = routing(T + N, T, k, E, skew)
+    orders = ORDERS[rng.integers(len(ORDERS))]
+    x = torch.from_numpy(rng.standard_normal((T if orders[0] == "token" else T * k, K))).to(torch.bfloat16)
+    codes, s, b = weights(rng, (E, N), K, fmt, group)
+    y = qm.grouped_matmul_packed(x.cuda(), *on_device((codes, s, b)), dev(off), perm=dev(perm), top_k=k, x_order=orders[0],
+                                 out_order=orders[1], out=torch.full((T * k, N), float("nan"), device="cuda"))
+    assert torch.isfinite(y).all()
+    if orders[1] == "slot":
+        y = y[dev(perm).long()]
+    rows, at = oracle.source_rows(x.double().numpy(), orders[0], perm, k), sampled(N)
+    for e in [*np.argsort(-np.diff(off))[:6], *rng.integers(0, E, 20), E - 1]:
+        r = slice(off[e], off[e + 1])
+        want, mag = oracle.matmul_packed(rows[r], codes[e][at], s[e][at], None if b is None else b[e][at])
+        close(y[r][:, torch.from_numpy(at).cuda()], want, tolerance(mag, K, group), "f32")
+
+
+@pytest.mark.parametrize("fmt,group", FORMATS)
+def test_scales_behind_a_row_are_not_its_own(fmt, group):
+    """Every second row's scales are no numbers: the rows between, whose blocks of scales reach into them, are as
+    without."""
+    N, K = 9000, 17 * 128 if group == 128 else 1120
+    K -= K % group
+    rng = np.random.default_rng(3)
+    x = torch.from_numpy(rng.standard_normal((3, K))).to(torch.bfloat16).cuda()
+    codes, s, b = weights(rng, (N,), K, fmt, group)
+    clean = qm.matmul_packed(x, *on_device((codes, s, b)), out_dtype="f32")
+    s[1::2] = 255 if fmt == "mxfp4" else np.nan
+    y = qm.matmul_packed(x, *on_device((codes, s, b)), out_dtype="f32")
+    assert torch.equal(y[:, ::2], clean[:, ::2]) and torch.isnan(y[:, 1::2]).all()
+
+
 def test_quantize_affine_feeds_it():
     """The framework's own converter, its int16 bit patterns passed on as they come."""
     g = torch.Generator().manual_seed(0)
