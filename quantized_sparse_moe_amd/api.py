@@ -750,17 +750,17 @@ def combine_rows_grad(dout: torch.Tensor, y: torch.Tensor, weights: torch.Tensor
     T, top_k = _slots(n, positions, _operand(weights, "weights", _F32, (2,), dev), None, dev)
     _rows(T, top_k, n, d)
     _shape(dout, "dout", (T, d))
+    _shape(weights, "weights", (T, top_k))
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return combine_rows_grad(dout, y, weights, positions, out, err)
-    w = _weights(weights, T, top_k, dev)
     dy = _out(out, (n, d), y.dtype, dev)
     if dy.dtype != y.dtype:
         raise TypeError(f"out must be {y.dtype} as y, got {dy.dtype}")
     dw = torch.empty(T, top_k, dtype=torch.float32, device=dev)
     check(_lib.load().moe_combine_rows_grad(
         dout.data_ptr(), _DT[dout.dtype], y.data_ptr(), _DT[y.dtype], n,
-        None if positions is None else positions.data_ptr(), w, T, top_k, d, dy.data_ptr(), dw.data_ptr(),
+        None if positions is None else positions.data_ptr(), weights.data_ptr(), T, top_k, d, dy.data_ptr(), dw.data_ptr(),
         _err_ptr(err, dev), _raw_stream(dev.index)), "moe_combine_rows_grad")
     return dy, dw
 

@@ -148,33 +148,49 @@ __device__ __forceinline__ float group_value(const uint32_t* v, int i) {
     return e8m0_to_f32((v[i / 4] >> (8 * (i % 4))) & 0xffu);
 }
 
-// The b-th expert with rows and its positions, offsets clamped to [0, n].
-// Uniform over the wave: 4 experts a lane, their count scanned.
-__device__ __forceinline__ bool find_bucket(const int32_t* offsets, int E, int n, int b, int* e, int* lo, int* hi) {
+// The b-th run of up to `most` rows of one expert: its expert, first position and
+// rows. Offsets are clamped to [0, n]; without them all rows are one expert's.
+// Uniform over the wave: 4 experts a lane, their runs scanned. So long buckets
+// take as many workgroups more as they have runs (280 tokens' top-7 of 214 experts
+// of 479 x 864, the most popular with 280 rows: 167 us with a bucket's runs one
+// after the other, @@RUNS@@ side by side).
+template <int MOST>
+__device__ __forceinline__ bool find_run(const int32_t* offsets, int E, int n, int b, int* e, int* first, int* rows) {
+  if (!offsets) {
+    *e = 0;
+    *first = b * MOST;
+    *rows = min(MOST, n - *first);
+    return *rows > 0;
+  }
   const int lane = lane_id();
   int before = 0;
   for (int e0 = 0; e0 < E; e0 += 256) {
     const int i = e0 + 4 * lane;
-    int o[5], sum = 0;
+    int o[5], runs[4], sum = 0;
 #pragma unroll
     for (int v = 0; v < 5; ++v) o[v] = min(max(offsets[min(i + v, E)], 0), n);
 #pragma unroll
-    for (int v = 0; v < 4; ++v) sum += o[v + 1] > o[v];
+    for (int v = 0; v < 4; ++v) {
+      runs[v] = (max(o[v + 1] - o[v], 0) + MOST - 1) / MOST;  // 0 past the last expert
+      sum += runs[v];
+    }
     const int incl = wave_scan(sum);
     const uint64_t m = __ballot(before + incl > b);
     if (m != 0) {
       const int src = __ffsll(static_cast<unsigned long long>(m)) - 1;
-      int at = before + __builtin_amdgcn_readlane(incl - sum, src);
+      int at = b - before - __builtin_amdgcn_readlane(incl - sum, src);  // run among the lane's
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        const int from = __builtin_amdgcn_readlane(o[v], src), to = __builtin_amdgcn_readlane(o[v + 1], src);
-        if (to > from && at++ == b) {
+        const int here = __builtin_amdgcn_readlane(runs[v], src);
+        if (at < here) {
           *e = e0 + 4 * src + v;
-          *lo = from;
-          *hi = to;
+          *first = __builtin_amdgcn_readlane(o[v], src) + at * MOST;
+          *rows = min(MOST, __builtin_amdgcn_readlane(o[v + 1], src) - *first);
           return true;
         }
+        at -= here;
       }
+      return false;
     }
     before += __builtin_amdgcn_readlane(incl, 63);
   }
@@ -257,11 +273,8 @@ __global__ __launch_bounds__(64 * kMostWaves) __attribute__((amdgpu_waves_per_eu
   const int groups = ((a.N + 15) / 16 + subs - 1) / subs;  // of tiles, one per `sub`
   const int total = a.T * a.k;
 
-  int e = 0, lo = blockIdx.y * kRows, hi = total, next_rows = gridDim.y * kRows;
-  if (a.offsets) {
-    if (!find_bucket(a.offsets, a.E, total, blockIdx.y, &e, &lo, &hi)) return;
-    next_rows = kRows;
-  }
+  int e, p0, rows;
+  if (!find_run<kRows>(a.offsets, a.E, total, blockIdx.y, &e, &p0, &rows)) return;
   const int steps = (a.K + kStep - 1) / kStep;
   const int value_bytes = a.K / a.group * Values::kSize;  // of a row
   const int64_t all_values = static_cast<int64_t>(a.E) * a.N * value_bytes;
@@ -295,173 +308,167 @@ __global__ __launch_bounds__(64 * kMostWaves) __attribute__((amdgpu_waves_per_eu
   char* values = lds + wave * kValueLds<FMT>;
   char* xs = lds + waves * kValueLds<FMT>;
   const int row_bytes = f.seg * kStepBytes + kPad, seg_groups = f.seg * kStepChunks * NG;
-  bool staged = false;
-  int buffer = 0;
-
-  for (int p0 = lo; p0 < hi; p0 += next_rows) {
-    const int rows = min(kRows, hi - p0);
-    float* sums = reinterpret_cast<float*>(xs + rows * row_bytes);
-    float* red = sums + (FMT == 0 ? rows * seg_groups : 0);
-    // where this lane finds its row of the left operand, and its rows' sums; the
-    // operand's other rows are row 0 again, and their results are not kept
-    const int from_row = x_row<VR>(n);
-    const int at = (from_row >= 0 && from_row < rows ? from_row : 0) * row_bytes + 16 * q;
-    int sum_at[VR];
+  float* sums = reinterpret_cast<float*>(xs + rows * row_bytes);
+  float* red = sums + (FMT == 0 ? rows * seg_groups : 0);
+  // where this lane finds its row of the left operand, and its rows' sums; the
+  // operand's other rows are row 0 again, and their results are not kept
+  const int from_row = x_row<VR>(n);
+  const int at = (from_row >= 0 && from_row < rows ? from_row : 0) * row_bytes + 16 * q;
+  int sum_at[VR];
 #pragma unroll
-    for (int v = 0; v < VR; ++v) sum_at[v] = min(4 * v + q, rows - 1) * seg_groups;
-    // x's columns of steps seg0 .. seg_end - 1: a workgroup's threads take
-    // neighbouring pieces of one row, several rows or runs of pieces in flight
-    auto stage = [&](int seg0, int seg_end) {
-      constexpr int kAhead = 2;
-      const int pieces = (seg_end - seg0) * (kStep / 8);
-      for (int r = 0, j0 = 0; j0 < pieces;) {
-        u32x4_t v[kAhead];
-        int to[kAhead];  // where a piece goes, -1: none
-        int sum_to[kAhead];
+  for (int v = 0; v < VR; ++v) sum_at[v] = min(4 * v + q, rows - 1) * seg_groups;
+  // x's columns of steps seg0 .. seg_end - 1: a workgroup's threads take
+  // neighbouring pieces of one row, several rows or runs of pieces in flight
+  auto stage = [&](int seg0, int seg_end) {
+    constexpr int kAhead = 2;
+    const int pieces = (seg_end - seg0) * (kStep / 8);
+    for (int r = 0, j0 = 0; j0 < pieces;) {
+      u32x4_t v[kAhead];
+      int to[kAhead];  // where a piece goes, -1: none
+      int sum_to[kAhead];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-          const int j = j0 + threadIdx.x;
-          to[u] = -1;
-          if (j < pieces) {
-            const int step = seg0 + j / (kStep / 8);
-            const int k = step * kStep + j % (kStep / 8) * 8;
-            const int row = max(row_of(a.perm, a.x_order, a.k, total, p0 + r, a.err), 0);
-            v[u] = u32x4_t{0, 0, 0, 0};
-            if (k < a.K)
-              v[u] = *reinterpret_cast<const u32x4_t*>(static_cast<const char*>(a.x) +
-                                                       2 * (static_cast<int64_t>(row) * a.K + k));
-            to[u] = r * row_bytes + 16 * j;
-            sum_to[u] = r * seg_groups + j / (16 / NG);
-          }
-          if (++r == rows) {
-            r = 0;
-            j0 += blockDim.x;
-          }
+      for (int u = 0; u < kAhead; ++u) {
+        const int j = j0 + threadIdx.x;
+        to[u] = -1;
+        if (j < pieces) {
+          const int step = seg0 + j / (kStep / 8);
+          const int k = step * kStep + j % (kStep / 8) * 8;
+          const int row = max(row_of(a.perm, a.x_order, a.k, total, p0 + r, a.err), 0);
+          v[u] = u32x4_t{0, 0, 0, 0};
+          if (k < a.K)
+            v[u] = *reinterpret_cast<const u32x4_t*>(static_cast<const char*>(a.x) +
+                                                     2 * (static_cast<int64_t>(row) * a.K + k));
+          to[u] = r * row_bytes + 16 * j;
+          sum_to[u] = r * seg_groups + j / (16 / NG);
         }
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-          if (to[u] < 0) continue;  // the same for a whole wave: pieces is a multiple of 64
-          *reinterpret_cast<u32x4_t*>(xs + to[u]) = in_code_order<FMT>(v[u]);
-          if constexpr (FMT == 0) {
-            float s = sum_of_8<TYPE>(v[u]);
-#pragma unroll
-            for (int o = 1; o < 16 / NG; o <<= 1) s += xchg(s, o);
-            if (lane % (16 / NG) == 0) sums[sum_to[u]] = s;
-          }
+        if (++r == rows) {
+          r = 0;
+          j0 += blockDim.x;
         }
       }
-    };
-
-    u32x4_t cur[kStepChunks], ahead[kStepChunks], next_s, next_b;
-    float acc[VR];
-    auto multiply = [&](int in_seg, int in_block) {
-      uint32_t s[Values::kStepBytes / 4], b[Values::kStepBytes / 4];
-      const char* v = values + n * kValueRow + in_block * Values::kStepBytes;
-      lds_words(v, s);
-      if constexpr (FMT == 0) lds_words(v + 16 * kValueRow, b);
 #pragma unroll
-      for (int h = 0; h < kStepChunks; ++h) {
-        __builtin_amdgcn_sched_barrier(0);  // chunk by chunk, for the registers
-        const u32x4_t w = quarters_together(cur[h]);
-        u32x4_t wf[4];
+      for (int u = 0; u < kAhead; ++u) {
+        if (to[u] < 0) continue;  // the same for a whole wave: pieces is a multiple of 64
+        *reinterpret_cast<u32x4_t*>(xs + to[u]) = in_code_order<FMT>(v[u]);
+        if constexpr (FMT == 0) {
+          float s = sum_of_8<TYPE>(v[u]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) wf[i] = codes_to_16<TYPE, FMT>(w[i]);
-        const char* xp = xs + at + in_seg * kStepBytes + h * 256;
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          f32x4_t d = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int i = 4 / NG * g; i < 4 / NG * (g + 1); ++i)
-            d = mma16<TYPE>(lds16(xp + 64 * i), wf[i], d);
-#pragma unroll
-          for (int r = 0; r < VR; ++r) {
-            acc[r] = fmaf(group_value<FMT>(s, h * NG + g), d[r], acc[r]);
-            if constexpr (FMT == 0)
-              acc[r] = fmaf(group_value<FMT>(b, h * NG + g), sums[sum_at[r] + (in_seg * kStepChunks + h) * NG + g],
-                            acc[r]);
-          }
+          for (int o = 1; o < 16 / NG; o <<= 1) s += xchg(s, o);
+          if (lane % (16 / NG) == 0) sums[sum_to[u]] = s;
         }
       }
-    };
-
-    const int first_group = blockIdx.x, turns = gridDim.x;
-    if (mine > 0) {
-      load_values(first_group, 0, next_s, next_b);
-      load_codes(first_group, 0, cur);
     }
-    for (int group = first_group; group < groups; group += turns) {
+  };
+
+  u32x4_t cur[kStepChunks], ahead[kStepChunks], next_s, next_b;
+  float acc[VR];
+  auto multiply = [&](int in_seg, int in_block) {
+    uint32_t s[Values::kStepBytes / 4], b[Values::kStepBytes / 4];
+    const char* v = values + n * kValueRow + in_block * Values::kStepBytes;
+    lds_words(v, s);
+    if constexpr (FMT == 0) lds_words(v + 16 * kValueRow, b);
 #pragma unroll
-      for (int v = 0; v < VR; ++v) acc[v] = 0.0f;
-      const int then = group + turns < groups ? group + turns : -1;
-      int i = 0;
-      for (int seg0 = 0; seg0 < steps; seg0 += f.seg) {
-        const int seg_end = min(seg0 + f.seg, steps);
-        if (f.seg < steps || group == first_group) {
-          if (staged) lds_barrier();  // the segment or the rows before have been read
-          stage(seg0, seg_end);
-          lds_barrier();
-          staged = true;
-        }
-        const int share = min(mine - i, f.own);
-        for (int j = 0; j < share; ++j, ++i) {
-          const int in_block = j % Values::kBlockSteps;
-          if (in_block == 0) {
-            // a wave's LDS accesses are made in order: only the compiler is held
-            __builtin_amdgcn_wave_barrier();
-            char* v = values + n * kValueRow + 16 * q;
-            if constexpr (!WHOLE) {
-              const int from = step_of(i) * Values::kStepBytes + 16 * q;
-              const int64_t left = all_values - w_row(group) * value_bytes;
-              next_s = within_row(next_s, from, value_bytes, left);
-              if constexpr (FMT == 0) next_b = within_row(next_b, from, value_bytes, left);
-            }
-            *reinterpret_cast<u32x4_t*>(v) = next_s;
-            if constexpr (FMT == 0) *reinterpret_cast<u32x4_t*>(v + 16 * kValueRow) = next_b;
-            __builtin_amdgcn_wave_barrier();
-            const int block = j + Values::kBlockSteps < share ? i + Values::kBlockSteps : i - j + share;
-            if (block < mine)
-              load_values(group, block, next_s, next_b);
-            else if (then >= 0)
-              load_values(then, 0, next_s, next_b);
-          }
-          const int in_seg = kpart * f.own + j, next_group = i + 1 < mine ? group : then;
-          if (next_group >= 0) {
-            load_codes(next_group, i + 1 < mine ? i + 1 : 0, ahead);
-            multiply(in_seg, in_block);
+    for (int h = 0; h < kStepChunks; ++h) {
+      __builtin_amdgcn_sched_barrier(0);  // chunk by chunk, for the registers
+      const u32x4_t w = quarters_together(cur[h]);
+      u32x4_t wf[4];
 #pragma unroll
-            for (int h = 0; h < kStepChunks; ++h) cur[h] = ahead[h];
-          } else {
-            multiply(in_seg, in_block);
-          }
+      for (int i = 0; i < 4; ++i) wf[i] = codes_to_16<TYPE, FMT>(w[i]);
+      const char* xp = xs + at + in_seg * kStepBytes + h * 256;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        f32x4_t d = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 4 / NG * g; i < 4 / NG * (g + 1); ++i)
+          d = mma16<TYPE>(lds16(xp + 64 * i), wf[i], d);
+#pragma unroll
+        for (int r = 0; r < VR; ++r) {
+          acc[r] = fmaf(group_value<FMT>(s, h * NG + g), d[r], acc[r]);
+          if constexpr (FMT == 0)
+            acc[r] = fmaf(group_value<FMT>(b, h * NG + g), sums[sum_at[r] + (in_seg * kStepChunks + h) * NG + g],
+                          acc[r]);
         }
       }
-      if (kw == 1) {
-        const int row_n = 16 * (group * subs + sub) + n;
+    }
+  };
+
+  const int first_group = blockIdx.x, turns = gridDim.x;
+  int buffer = 0;
+  if (mine > 0) {
+    load_values(first_group, 0, next_s, next_b);
+    load_codes(first_group, 0, cur);
+  }
+  for (int group = first_group; group < groups; group += turns) {
 #pragma unroll
-        for (int v = 0; v < VR; ++v) {
-          const int r = 4 * v + q;
-          if (r >= rows || row_n >= a.N) continue;
-          const int row = row_of(a.perm, a.out_order, a.k, total, p0 + r, a.err);
-          if (row >= 0) store_value(a, row, row_n, acc[v]);
-        }
-        continue;
+    for (int v = 0; v < VR; ++v) acc[v] = 0.0f;
+    const int then = group + turns < groups ? group + turns : -1;
+    int i = 0;
+    for (int seg0 = 0; seg0 < steps; seg0 += f.seg) {
+      const int seg_end = min(seg0 + f.seg, steps);
+      if (f.seg < steps || group == first_group) {
+        if (seg0 != 0 || group != first_group) lds_barrier();  // the segment before has been read
+        stage(seg0, seg_end);
+        lds_barrier();
       }
-      // the waves' parts, joined in their order; two buffers in turn, so that
-      // one barrier does
-      float* part = red + buffer * waves * rows * 16;
-      buffer ^= 1;
+      const int share = min(mine - i, f.own);
+      for (int j = 0; j < share; ++j, ++i) {
+        const int in_block = j % Values::kBlockSteps;
+        if (in_block == 0) {
+          // a wave's LDS accesses are made in order: only the compiler is held
+          __builtin_amdgcn_wave_barrier();
+          char* v = values + n * kValueRow + 16 * q;
+          if constexpr (!WHOLE) {
+            const int from = step_of(i) * Values::kStepBytes + 16 * q;
+            const int64_t left = all_values - w_row(group) * value_bytes;
+            next_s = within_row(next_s, from, value_bytes, left);
+            if constexpr (FMT == 0) next_b = within_row(next_b, from, value_bytes, left);
+          }
+          *reinterpret_cast<u32x4_t*>(v) = next_s;
+          if constexpr (FMT == 0) *reinterpret_cast<u32x4_t*>(v + 16 * kValueRow) = next_b;
+          __builtin_amdgcn_wave_barrier();
+          const int block = j + Values::kBlockSteps < share ? i + Values::kBlockSteps : i - j + share;
+          if (block < mine)
+            load_values(group, block, next_s, next_b);
+          else if (then >= 0)
+            load_values(then, 0, next_s, next_b);
+        }
+        const int in_seg = kpart * f.own + j, next_group = i + 1 < mine ? group : then;
+        if (next_group >= 0) {
+          load_codes(next_group, i + 1 < mine ? i + 1 : 0, ahead);
+          multiply(in_seg, in_block);
 #pragma unroll
-      for (int v = 0; v < VR; ++v)
-        if (4 * v + q < rows) part[(wave * rows + 4 * v + q) * 16 + n] = acc[v];
-      lds_barrier();
-      for (int i = threadIdx.x; i < subs * rows * 16; i += blockDim.x) {
-        const int col = i % 16, r = i / 16 % rows, of = i / 16 / rows, row_n = 16 * (group * subs + of) + col;
-        if (row_n >= a.N) continue;
-        float v = 0.0f;
-        for (int w = 0; w < kw; ++w) v += part[((of * kw + w) * rows + r) * 16 + col];
+          for (int h = 0; h < kStepChunks; ++h) cur[h] = ahead[h];
+        } else {
+          multiply(in_seg, in_block);
+        }
+      }
+    }
+    if (kw == 1) {
+      const int row_n = 16 * (group * subs + sub) + n;
+#pragma unroll
+      for (int v = 0; v < VR; ++v) {
+        const int r = 4 * v + q;
+        if (r >= rows || row_n >= a.N) continue;
         const int row = row_of(a.perm, a.out_order, a.k, total, p0 + r, a.err);
-        if (row >= 0) store_value(a, row, row_n, v);
+        if (row >= 0) store_value(a, row, row_n, acc[v]);
       }
+      continue;
+    }
+    // the waves' parts, joined in their order; two buffers in turn, so that
+    // one barrier does
+    float* part = red + buffer * waves * rows * 16;
+    buffer ^= 1;
+#pragma unroll
+    for (int v = 0; v < VR; ++v)
+      if (4 * v + q < rows) part[(wave * rows + 4 * v + q) * 16 + n] = acc[v];
+    lds_barrier();
+    for (int i = threadIdx.x; i < subs * rows * 16; i += blockDim.x) {
+      const int col = i % 16, r = i / 16 % rows, of = i / 16 / rows, row_n = 16 * (group * subs + of) + col;
+      if (row_n >= a.N) continue;
+      float v = 0.0f;
+      for (int w = 0; w < kw; ++w) v += part[((of * kw + w) * rows + r) * 16 + col];
+      const int row = row_of(a.perm, a.out_order, a.k, total, p0 + r, a.err);
+      if (row >= 0) store_value(a, row, row_n, v);
     }
   }
 }
@@ -703,11 +710,8 @@ __global__ __launch_bounds__(64 * kMostWaves) void k_small(const PackedArgs a) {
   const int lane = lane_id(), n = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
   const int total = a.T * a.k, n0 = 16 * blockIdx.x;
-  int e = 0, lo = blockIdx.y * kRows, hi = total, next = gridDim.y * kRows;
-  if (a.offsets) {
-    if (!find_bucket(a.offsets, a.E, total, blockIdx.y, &e, &lo, &hi)) return;
-    next = kRows;
-  }
+  int e, p0, rows;
+  if (!find_run<kRows>(a.offsets, a.E, total, blockIdx.y, &e, &p0, &rows)) return;
   const int G = a.K / a.group, chunks = (a.K + kChunk - 1) / kChunk;
   const int64_t w_row = static_cast<int64_t>(e) * a.N + min(n0 + n, a.N - 1);
   const char* codes = reinterpret_cast<const char*>(a.codes) + w_row * (a.K / 2);
@@ -716,57 +720,54 @@ __global__ __launch_bounds__(64 * kMostWaves) void k_small(const PackedArgs a) {
   // a share of neighbouring chunks for each wave, four at a time
   constexpr int kTogether = 4;
   const int share = (chunks + kMostWaves - 1) / kMostWaves, c0 = min(wave * share, chunks), c1 = min(c0 + share, chunks);
-  for (int p0 = lo; p0 < hi; p0 += next) {
-    const int rows = min(kRows, hi - p0), mine = x_row<1>(n);
-    const int p = p0 + (mine >= 0 && mine < rows ? mine : 0);
-    const char* x = static_cast<const char*>(a.x) +
-                    2 * static_cast<int64_t>(max(row_of(a.perm, a.x_order, a.k, total, p, a.err), 0)) * a.K;
-    float acc = 0.0f;
-    for (int c = c0; c < c1; c += kTogether) {
-      Chunk<FMT, NG> w[kTogether];
-      u32x4_t xv[kTogether][4];
+  const int mine = x_row<1>(n);
+  const int p = p0 + (mine >= 0 && mine < rows ? mine : 0);
+  const char* x = static_cast<const char*>(a.x) +
+                  2 * static_cast<int64_t>(max(row_of(a.perm, a.x_order, a.k, total, p, a.err), 0)) * a.K;
+  float acc = 0.0f;
+  for (int c = c0; c < c1; c += kTogether) {
+    Chunk<FMT, NG> w[kTogether];
+    u32x4_t xv[kTogether][4];
 #pragma unroll
-      for (int u = 0; u < kTogether; ++u) {
-        const int at = min(c + u, c1 - 1);
-        w[u] = load_chunk<FMT, NG>(codes, scales, biases, at, q, a.K, G);
+    for (int u = 0; u < kTogether; ++u) {
+      const int at = min(c + u, c1 - 1);
+      w[u] = load_chunk<FMT, NG>(codes, scales, biases, at, q, a.K, G);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int k = at * kChunk + 32 * i + 8 * q;
-          xv[u][i] = *reinterpret_cast<const u32x4_t*>(x + 2 * min(k, a.K - 8));
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kTogether; ++u) {
-        w[u].settle(min(c + u, c1 - 1), G);
-        const u32x4_t together = quarters_together(w[u].w);
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          f32x4_t d = {0.0f, 0.0f, 0.0f, 0.0f}, sx = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int i = 4 / NG * g; i < 4 / NG * (g + 1); ++i) {
-            // pieces past the row's end, and of a chunk taken twice, count as zeros
-            const bool there = (c + u) * kChunk + 32 * i + 8 * q < a.K && c + u < c1;
-            const u32x4_t xf = in_code_order<FMT>(there ? xv[u][i] : u32x4_t{0, 0, 0, 0});
-            d = mma16<TYPE>(xf, codes_to_16<TYPE, FMT>(together[i]), d);
-            if constexpr (FMT == 0) sx = mma16<TYPE>(xf, ones_16<TYPE>(), sx);
-          }
-          acc = fmaf(chunk_value<FMT, NG>(w[u].s, g), d[0], acc);
-          if constexpr (FMT == 0) acc = fmaf(chunk_value<FMT, NG>(w[u].b, g), sx[0], acc);
-        }
+      for (int i = 0; i < 4; ++i) {
+        const int k = at * kChunk + 32 * i + 8 * q;
+        xv[u][i] = *reinterpret_cast<const u32x4_t*>(x + 2 * min(k, a.K - 8));
       }
     }
-    if (p0 != lo) lds_barrier();
-    red[wave][q][n] = acc;
-    lds_barrier();
-    for (int i = threadIdx.x; i < rows * 16; i += 64 * kMostWaves) {
-      const int col = i % 16, r = i / 16;
-      if (n0 + col >= a.N) continue;
-      float v = 0.0f;
 #pragma unroll
-      for (int j = 0; j < kMostWaves; ++j) v += red[j][r][col];
-      const int row = row_of(a.perm, a.out_order, a.k, total, p0 + r, a.err);
-      if (row >= 0) store_value(a, row, n0 + col, v);
+    for (int u = 0; u < kTogether; ++u) {
+      w[u].settle(min(c + u, c1 - 1), G);
+      const u32x4_t together = quarters_together(w[u].w);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        f32x4_t d = {0.0f, 0.0f, 0.0f, 0.0f}, sx = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 4 / NG * g; i < 4 / NG * (g + 1); ++i) {
+          // pieces past the row's end, and of a chunk taken twice, count as zeros
+          const bool there = (c + u) * kChunk + 32 * i + 8 * q < a.K && c + u < c1;
+          const u32x4_t xf = in_code_order<FMT>(there ? xv[u][i] : u32x4_t{0, 0, 0, 0});
+          d = mma16<TYPE>(xf, codes_to_16<TYPE, FMT>(together[i]), d);
+          if constexpr (FMT == 0) sx = mma16<TYPE>(xf, ones_16<TYPE>(), sx);
+        }
+        acc = fmaf(chunk_value<FMT, NG>(w[u].s, g), d[0], acc);
+        if constexpr (FMT == 0) acc = fmaf(chunk_value<FMT, NG>(w[u].b, g), sx[0], acc);
+      }
     }
+  }
+  red[wave][q][n] = acc;
+  lds_barrier();
+  for (int i = threadIdx.x; i < rows * 16; i += 64 * kMostWaves) {
+    const int col = i % 16, r = i / 16;
+    if (n0 + col >= a.N) continue;
+    float v = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kMostWaves; ++j) v += red[j][r][col];
+    const int row = row_of(a.perm, a.out_order, a.k, total, p0 + r, a.err);
+    if (row >= 0) store_value(a, row, n0 + col, v);
   }
 }
 
@@ -840,12 +841,27 @@ hipError_t launch_short(const PackedArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Runs of up to `most` rows that the buckets can have together (find_run).
+int64_t most_runs(const PackedArgs& a, int most) {
+  const int64_t n = static_cast<int64_t>(a.T) * a.k;
+  return a.offsets ? std::min<int64_t>(n, a.E) + n / most : (n + most - 1) / most;
+}
+constexpr int64_t kMostY = 65535;
+
+// More than the default 64 KiB of dynamic LDS, allowed once for each kernel.
+template <auto KERNEL>
+hipError_t allow_lds() {
+  static const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(KERNEL),
+                                                  hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+  return e;
+}
+
 template <int TYPE, int FMT, int NG, int VR>
 hipError_t launch_few(const PackedArgs& a, hipStream_t s) {
   constexpr int kRows = 4 * VR;
   const int n = a.T * a.k, steps = (a.K + kStep - 1) / kStep, rows = std::min(kRows, n);
   const int64_t tiles = (a.N + 15) / 16;
-  const int64_t y = std::min(a.offsets ? std::min(n, a.E) : (n + kRows - 1) / kRows, 65535);
+  const int64_t y = most_runs(a, kRows);
   const int step_bytes = rows * (2 * kStep + (FMT == 0 ? kStepChunks * NG * 4 : 0));
   // LDS beside the steps of x
   auto fixed = [&](int waves, int kw) {
@@ -867,27 +883,25 @@ hipError_t launch_few(const PackedArgs& a, hipStream_t s) {
   // times as many where buckets may be empty or long.
   const int64_t at_once = 256 * per_cu * (y > 8 ? 4 : 1), turns = (groups * y + at_once - 1) / at_once;
   const int64_t gx = (groups + turns - 1) / turns;
-  if (gx * y > max_workgroups(64 * kMostWaves)) return hipErrorInvalidValue;
+  if (y > kMostY || gx * y > max_workgroups(64 * kMostWaves)) return hipErrorInvalidValue;
   const size_t lds = fixed(waves, kw) + static_cast<size_t>(seg) * step_bytes;
-  auto launch = [&](auto kernel) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
-    if (e != hipSuccess) return e;
+  auto launch = [&](hipError_t allowed, auto kernel) {
+    if (allowed != hipSuccess) return allowed;
     QSMOE_LAUNCH(kernel, dim3(static_cast<unsigned>(gx), static_cast<unsigned>(y)), dim3(64 * waves), lds, s, a,
                  FewShape{kw_log2, seg, own});
     return hipGetLastError();
   };
   // pieces start at multiples of 16 bytes too: of the steps of 8 bytes at even ones
   const bool even = Groups<FMT, NG>::kStepBytes >= 16 || own % 2 == 0 || (kw == 1 && seg >= steps);
-  if (a.K / a.group * Groups<FMT, NG>::kSize % 16 == 0 && even) return launch(k_few_rows<TYPE, FMT, NG, VR, true>);
-  return launch(k_few_rows<TYPE, FMT, NG, VR, false>);
+  if (a.K / a.group * Groups<FMT, NG>::kSize % 16 == 0 && even)
+    return launch(allow_lds<k_few_rows<TYPE, FMT, NG, VR, true>>(), k_few_rows<TYPE, FMT, NG, VR, true>);
+  return launch(allow_lds<k_few_rows<TYPE, FMT, NG, VR, false>>(), k_few_rows<TYPE, FMT, NG, VR, false>);
 }
 
 template <int TYPE, int FMT, int NG>
 hipError_t launch_small(const PackedArgs& a, hipStream_t s) {
-  const int64_t n = static_cast<int64_t>(a.T) * a.k, tiles = (a.N + 15) / 16;
-  const int64_t y = std::min<int64_t>(a.offsets ? std::min<int64_t>(n, a.E) : (n + 3) / 4, 65535);
-  if (tiles * y > max_workgroups(64 * kMostWaves)) return hipErrorInvalidValue;
+  const int64_t tiles = (a.N + 15) / 16, y = most_runs(a, 4);
+  if (y > kMostY || tiles * y > max_workgroups(64 * kMostWaves)) return hipErrorInvalidValue;
   QSMOE_LAUNCH((k_small<TYPE, FMT, NG>), dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(y)),
                dim3(64 * kMostWaves), 0, s, a);
   return hipGetLastError();
@@ -904,10 +918,7 @@ hipError_t launch_many(const PackedArgs& a, hipStream_t s) {
   if (pairs > max_workgroups(64 * kMostWaves)) return hipErrorInvalidValue;
   constexpr size_t lds = std::max<size_t>(2 * KW * CH * BM * kManyPitch, KW == 1 ? 0 : kMostWaves * BM * 16 * RT * 4);
   static_assert(lds <= kLds, "LDS of a CU");
-  static const hipError_t attr = hipFuncSetAttribute(
-      reinterpret_cast<const void*>(k_many_rows<TYPE, FMT, NG, AB, RT, CH, KW>), hipFuncAttributeMaxDynamicSharedMemorySize,
-      kLds);
-  if (attr != hipSuccess) return attr;
+  if (const hipError_t e = allow_lds<k_many_rows<TYPE, FMT, NG, AB, RT, CH, KW>>(); e != hipSuccess) return e;
   QSMOE_LAUNCH((k_many_rows<TYPE, FMT, NG, AB, RT, CH, KW>), dim3(static_cast<unsigned>(pairs)), dim3(64 * kMostWaves), lds,
                s, a, ctiles, run);
   return hipGetLastError();

