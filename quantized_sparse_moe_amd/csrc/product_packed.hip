@@ -17,7 +17,8 @@
 //
 // Three kernels: k_few_rows streams a matrix past up to 16 rows of x in LDS,
 // k_many_rows goes over it with tiles of 16 to 64 rows, k_small is for products
-// that end before a stream has begun.
+// that end before a stream has begun. k_short_rows takes contractions shorter than
+// a chunk.
 #include <algorithm>
 
 #include "elements.hpp"
@@ -153,7 +154,7 @@ __device__ __forceinline__ float group_value(const uint32_t* v, int i) {
 // Uniform over the wave: 4 experts a lane, their runs scanned. So long buckets
 // take as many workgroups more as they have runs (280 tokens' top-7 of 214 experts
 // of 479 x 864, the most popular with 280 rows: 167 us with a bucket's runs one
-// after the other, @@RUNS@@ side by side).
+// after the other, 35 side by side).
 template <int MOST>
 __device__ __forceinline__ bool find_run(const int32_t* offsets, int E, int n, int b, int* e, int* first, int* rows) {
   if (!offsets) {
@@ -254,14 +255,16 @@ struct FewShape {
 // 4096, groups of 64: 72 to 77 us so, 61 to 65 in blocks). Their lanes meet the
 // multiplying ones through the wave's own part of LDS.
 //
-// HBM bounds it: 129280 x 4096 with one row 61 to 65 us, 4.6 to 4.9 TB/s; 64
-// tokens' top-6 of 256 experts of 4096 x 4096 324 us, 5.3 TB/s of the experts
-// used. Loads that bypass the caches are 2 to 6 % slower. A third wave to a SIMD
-// is worth the registers that it costs.
+// HBM bounds it: 129280 x 4096 with one row 57 to 65 us, 4.6 to 5.2 TB/s; 64
+// tokens' top-6 of 256 experts of 4096 x 4096 314 us, 5.4 TB/s of the experts
+// used; 512 tokens (12 rows a bucket, several runs where it is popular) 634. Loads
+// that bypass the caches are 2 to 6 % slower. A third wave to a SIMD is worth the
+// registers that it costs.
 // WHOLE: a row's values and the steps at which a wave's blocks of them begin are
 // multiples of 16 bytes, so that none of the pieces ends behind its row.
 template <int TYPE, int FMT, int NG, int VR, bool WHOLE>
-__global__ __launch_bounds__(64 * kMostWaves) __attribute__((amdgpu_waves_per_eu(3))) void k_few_rows(const PackedArgs a, const FewShape f) {
+__global__ __launch_bounds__(64 * kMostWaves) __attribute__((amdgpu_waves_per_eu(3)))
+void k_few_rows(const PackedArgs a, const FewShape f) {
   using Values = Groups<FMT, NG>;
   constexpr int kRows = 4 * VR;
   constexpr int kStepBytes = 2 * kStep;
@@ -478,7 +481,8 @@ __global__ __launch_bounds__(64 * kMostWaves) __attribute__((amdgpu_waves_per_eu
 // row's G groups allow, and moved to their place when used (here the shift would
 // wait for them).
 template <int FMT, int NG>
-using chunk_values_t = std::conditional_t<FMT == 1 || NG == 2, uint32_t, std::conditional_t<NG == 4, uint64_t, uint16_t>>;
+using chunk_values_t =
+    std::conditional_t<FMT == 1 || NG == 2, uint32_t, std::conditional_t<NG == 4, uint64_t, uint16_t>>;
 
 template <int FMT, int NG>
 __device__ __forceinline__ chunk_values_t<FMT, NG> load_chunk_values(const char* row, int c, int G) {
@@ -719,7 +723,8 @@ __global__ __launch_bounds__(64 * kMostWaves) void k_small(const PackedArgs a) {
   const char* biases = FMT == 0 ? reinterpret_cast<const char*>(a.biases) + w_row * G * 2 : nullptr;
   // a share of neighbouring chunks for each wave, four at a time
   constexpr int kTogether = 4;
-  const int share = (chunks + kMostWaves - 1) / kMostWaves, c0 = min(wave * share, chunks), c1 = min(c0 + share, chunks);
+  const int share = (chunks + kMostWaves - 1) / kMostWaves;
+  const int c0 = min(wave * share, chunks), c1 = min(c0 + share, chunks);
   const int mine = x_row<1>(n);
   const int p = p0 + (mine >= 0 && mine < rows ? mine : 0);
   const char* x = static_cast<const char*>(a.x) +
@@ -785,7 +790,8 @@ __global__ __launch_bounds__(256) void k_short_rows(const PackedArgs a) {
     if (e < 0 || n >= a.N) continue;
     const int64_t w = static_cast<int64_t>(e) * a.N + n;
     const int row = max(row_of(a.perm, a.x_order, a.k, total, p, a.err), 0);
-    const uint4* x = reinterpret_cast<const uint4*>(static_cast<const char*>(a.x) + 2 * static_cast<int64_t>(row) * a.K);
+    const uint4* x =
+        reinterpret_cast<const uint4*>(static_cast<const char*>(a.x) + 2 * static_cast<int64_t>(row) * a.K);
     float acc = 0.0f;
     for (int g = 0; g < G; ++g) {
       float dot = 0.0f, sum = 0.0f;
@@ -820,10 +826,10 @@ __global__ __launch_bounds__(256) void k_short_rows(const PackedArgs a) {
 
 // Which kernel, measured on both sides (bf16, groups of 64, weights of 4096 x 4096
 // unless said):
-//  - Buckets of more than 16 rows on average go to k_many_rows: 200 tokens' top-8
-//    of 100 experts of 1408 x 2048 (16 rows) 126 us there and 137 with k_few_rows,
-//    but 512 tokens' top-6 of 256 experts (12 rows) 1200 and 950, one matrix of
-//    32768 x 4096 with 16 rows 44 and 28.
+//  - Buckets of more than 20 rows on average go to k_many_rows. k_few_rows and
+//    k_many_rows: 18 rows of each of 64 experts (groups of 128) 212 and 251 us, 24
+//    rows 270 and 252; 18 rows of 16 experts of 2048 x 2048 33 and 39 us, 32 rows 51
+//    and 42; 512 tokens' top-6 of 256 experts (12 rows) 634 and 1200.
 //  - Up to 512 tiles of 16 rows of W, all buckets together, are no stream: up to 4
 //    rows k_small (7.5 us; k_few_rows 8.2, k_many_rows 13), from 5 on k_many_rows
 //    (13 rows of 2053 x 4000, groups of 32: 8.1 us; with all of x in registers as in
@@ -831,7 +837,7 @@ __global__ __launch_bounds__(256) void k_short_rows(const PackedArgs a) {
 //    16 with k_few_rows.
 //  - Tiles of k_many_rows are as wide as leaves 192 workgroups (64 rows of 32768 x
 //    8192, groups of 128: 118 us; 143 with 400, 207 with 96).
-constexpr int64_t kSmallTiles = 512, kEnoughGroups = 192;
+constexpr int64_t kFewRows = 20, kSmallTiles = 512, kEnoughGroups = 192;
 
 template <int TYPE, int FMT>
 hipError_t launch_short(const PackedArgs& a, hipStream_t s) {
@@ -868,7 +874,8 @@ hipError_t launch_few(const PackedArgs& a, hipStream_t s) {
     return rows * kPad + waves * kValueLds<FMT> + (kw == 1 ? 0 : 2 * waves * rows * 16 * 4);
   };
   // Small workgroups, three to a CU, where x and the parts leave them the room
-  // (a token's six experts of 4096 x 4096: 16 us; 18 with one of 8 waves).
+  // (a token's six experts of 4096 x 4096: 16 us; 18 with one of 8 waves; four to a
+  // CU are no faster).
   const int waves = fixed(4, 4) + steps * step_bytes <= kLds / 3 ? 4 : 8, per_cu = waves == 4 ? 3 : 1;
   // As few waves to a contraction as still give every wave a tile.
   int kw_log2 = 0;
@@ -919,8 +926,8 @@ hipError_t launch_many(const PackedArgs& a, hipStream_t s) {
   constexpr size_t lds = std::max<size_t>(2 * KW * CH * BM * kManyPitch, KW == 1 ? 0 : kMostWaves * BM * 16 * RT * 4);
   static_assert(lds <= kLds, "LDS of a CU");
   if (const hipError_t e = allow_lds<k_many_rows<TYPE, FMT, NG, AB, RT, CH, KW>>(); e != hipSuccess) return e;
-  QSMOE_LAUNCH((k_many_rows<TYPE, FMT, NG, AB, RT, CH, KW>), dim3(static_cast<unsigned>(pairs)), dim3(64 * kMostWaves), lds,
-               s, a, ctiles, run);
+  QSMOE_LAUNCH((k_many_rows<TYPE, FMT, NG, AB, RT, CH, KW>), dim3(static_cast<unsigned>(pairs)),
+               dim3(64 * kMostWaves), lds, s, a, ctiles, run);
   return hipGetLastError();
 }
 
@@ -942,7 +949,7 @@ hipError_t pick_rows(const PackedArgs& a, hipStream_t s) {
   // rows of a bucket: on average over all experts, and of the longer ones, roughly
   const int64_t buckets = a.offsets ? std::min<int64_t>(n, a.E) : 1, average = (n + buckets - 1) / buckets;
   const int64_t rows = a.offsets ? std::min(n, 2 * n / a.E + 2) : n;
-  if (average <= 16 && tiles * buckets > kSmallTiles)
+  if (average <= kFewRows && tiles * buckets > kSmallTiles)
     return rows <= 8 ? launch_few<TYPE, FMT, NG, 2>(a, s) : launch_few<TYPE, FMT, NG, 4>(a, s);
   if (rows <= 4) return launch_small<TYPE, FMT, NG>(a, s);
   if (average <= 16) return pick_many<TYPE, FMT, NG, 1>(a, buckets, s);

@@ -39,8 +39,8 @@ __global__ __launch_bounds__(1024) void k_invert_owned(const int32_t* __restrict
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) {
       const int p = p0 + 4096 * i;
+      r[i] = {};
       if (p < n) r[i] = load_raw<kF32, 4>(reinterpret_cast<const char*>(perm + p), n - p);
-      else r[i] = {};
     }
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) {
@@ -60,7 +60,8 @@ __global__ __launch_bounds__(1024) void k_invert_owned(const int32_t* __restrict
 // Of longer lists every workgroup would read too much: the same in two
 // launches, with atomics on memory (a maximum, whose order does not matter).
 __global__ __launch_bounds__(256) void k_invert_fill(int size, int32_t* __restrict__ positions) {
-  for (int64_t i = blockIdx.x * int64_t{256} + threadIdx.x; i < size; i += gridDim.x * int64_t{256}) positions[i] = -1;
+  for (int64_t i = blockIdx.x * int64_t{256} + threadIdx.x; i < size; i += gridDim.x * int64_t{256})
+    positions[i] = -1;
 }
 __global__ __launch_bounds__(256) void k_invert_scatter(const int32_t* __restrict__ perm, int n, int size,
                                                         int32_t* __restrict__ positions, int32_t* err) {
@@ -160,7 +161,8 @@ __global__ __launch_bounds__(256) void k_combine_rows(const CombineArgs g, const
         w[i] = 1.0f;
         if (there[i]) {
           if (g.w) w[i] = g.w[a];
-          r[i] = load_raw<IN, V>(static_cast<const char*>(g.y) + (static_cast<int64_t>(p) * g.d + at) * kElemBytes<IN>, left);
+          r[i] = load_raw<IN, V>(
+              static_cast<const char*>(g.y) + (static_cast<int64_t>(p) * g.d + at) * kElemBytes<IN>, left);
         }
       }
 #pragma unroll
@@ -211,7 +213,8 @@ __device__ __forceinline__ float combine_grad_row(const CombineGradArgs& g, int6
 // 2^shift lanes of a wave per assignment: 4096 tokens, top-8, rows of 64 3.7 us
 // (29 with a workgroup each), top-2 of 1003 10.5 (18).
 template <int IN, int DOUT>
-__global__ __launch_bounds__(256) void k_combine_grad(const CombineGradArgs g, const int shift, const int64_t blocks) {
+__global__ __launch_bounds__(256) void k_combine_grad(const CombineGradArgs g, const int shift,
+                                                      const int64_t blocks) {
   const int lane = threadIdx.x & ((1 << shift) - 1);
   for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
     const int64_t a = b * (256 >> shift) + (threadIdx.x >> shift);
@@ -259,7 +262,8 @@ hipError_t launch_gather_rows(const GatherArgs& g, hipStream_t s) {
       // Slices for every XCD, a result larger than the eight L2s of 4 MB (smaller ones
       // are the next kernel's to find there), and a grid that holds them.
       constexpr int shift = 5;
-      const int slices = (g.d + (V << shift) - 1) / (V << shift), per_slice = (g.n + (256 >> shift) - 1) / (256 >> shift);
+      const int slices = (g.d + (V << shift) - 1) / (V << shift);
+      const int per_slice = (g.n + (256 >> shift) - 1) / (256 >> shift);
       const int64_t out_bytes = static_cast<int64_t>(g.n) * g.d * kElemBytes<OUT>;
       const int64_t groups = static_cast<int64_t>((slices + 7) / 8 * 8) * per_slice;
       if (out_bytes > (int64_t{32} << 20) && slices >= 8 && groups <= max_workgroups(256)) {
