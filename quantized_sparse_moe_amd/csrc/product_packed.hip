@@ -20,6 +20,7 @@
 // that end before a stream has begun. k_short_rows takes contractions shorter than
 // a chunk.
 #include <algorithm>
+#include <atomic>
 
 #include "elements.hpp"
 #include "kernels.hpp"
@@ -854,11 +855,18 @@ int64_t most_runs(const PackedArgs& a, int most) {
 }
 constexpr int64_t kMostY = 65535;
 
-// More than the default 64 KiB of dynamic LDS, allowed once for each kernel.
+// More than the default 64 KiB of dynamic LDS, allowed once for each kernel and
+// device.
 template <auto KERNEL>
 hipError_t allow_lds() {
-  static const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(KERNEL),
-                                                  hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+  static std::atomic<uint64_t> allowed{0};
+  int device = 0;
+  if (const hipError_t e = hipGetDevice(&device); e != hipSuccess) return e;
+  const uint64_t bit = device < 64 ? uint64_t{1} << device : 0;
+  if (allowed.load(std::memory_order_relaxed) & bit) return hipSuccess;
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(KERNEL),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+  if (e == hipSuccess) allowed.fetch_or(bit, std::memory_order_relaxed);
   return e;
 }
 

@@ -228,7 +228,8 @@ __global__ __launch_bounds__(256) void k_combine_grad(const CombineGradArgs g, c
 }
 
 // A workgroup per assignment, where there are few long rows: 366 of 4096 4.5 us,
-// 6.8 with a wave each; from 1500 on a wave each is as fast, at 3072 11.4 us (14).
+// 6.8 with a wave each; from 1500 on a wave each is as fast, and with more of them
+// faster.
 template <int IN, int DOUT>
 __global__ __launch_bounds__(256) void k_combine_grad_few(const CombineGradArgs g) {
   __shared__ float part[4];
