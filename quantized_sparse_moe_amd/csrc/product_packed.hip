@@ -156,12 +156,12 @@ __device__ __forceinline__ float group_value(const uint32_t* v, int i) {
 // take as many workgroups more as they have runs (280 tokens' top-7 of 214 experts
 // of 479 x 864, the most popular with 280 rows: 167 us with a bucket's runs one
 // after the other, 35 side by side).
-template <int MOST>
-__device__ __forceinline__ bool find_run(const int32_t* offsets, int E, int n, int b, int* e, int* first, int* rows) {
+__device__ __forceinline__ bool find_run(const int32_t* offsets, int E, int n, int b, int most, int* e, int* first,
+                                         int* rows) {
   if (!offsets) {
     *e = 0;
-    *first = b * MOST;
-    *rows = min(MOST, n - *first);
+    *first = b * most;
+    *rows = min(most, n - *first);
     return *rows > 0;
   }
   const int lane = lane_id();
@@ -173,7 +173,8 @@ __device__ __forceinline__ bool find_run(const int32_t* offsets, int E, int n, i
     for (int v = 0; v < 5; ++v) o[v] = min(max(offsets[min(i + v, E)], 0), n);
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      runs[v] = (max(o[v + 1] - o[v], 0) + MOST - 1) / MOST;  // 0 past the last expert
+      const uint32_t len = max(o[v + 1] - o[v], 0);  // 0 past the last expert
+      runs[v] = (len + most - 1) / static_cast<uint32_t>(most);
       sum += runs[v];
     }
     const int incl = wave_scan(sum);
@@ -186,8 +187,8 @@ __device__ __forceinline__ bool find_run(const int32_t* offsets, int E, int n, i
         const int here = __builtin_amdgcn_readlane(runs[v], src);
         if (at < here) {
           *e = e0 + 4 * src + v;
-          *first = __builtin_amdgcn_readlane(o[v], src) + at * MOST;
-          *rows = min(MOST, __builtin_amdgcn_readlane(o[v + 1], src) - *first);
+          *first = __builtin_amdgcn_readlane(o[v], src) + at * most;
+          *rows = min(most, __builtin_amdgcn_readlane(o[v + 1], src) - *first);
           return true;
         }
         at -= here;
@@ -241,11 +242,11 @@ __device__ __forceinline__ int x_row(int m) {
   return m % 4 < VR ? m % 4 * 4 + m / 4 : -1;
 }
 
-// How a launch is laid out: 2^kw_log2 of a workgroup's waves share a tile's
-// contraction, `own` steps each of every segment of `seg` steps, as much of x as
-// fits in LDS.
+// How a launch is laid out: runs of up to `most` rows; 2^kw_log2 of a workgroup's
+// waves share a tile's contraction, `own` steps each of every segment of `seg` steps,
+// as much of x as fits in LDS.
 struct FewShape {
-  int32_t kw_log2, seg, own;
+  int32_t most, kw_log2, seg, own;
 };
 
 // A tile is 16 rows of W. A workgroup keeps its rows of x (4 VR at a time) in LDS
@@ -267,7 +268,6 @@ template <int TYPE, int FMT, int NG, int VR, bool WHOLE>
 __global__ __launch_bounds__(64 * kMostWaves) __attribute__((amdgpu_waves_per_eu(3)))
 void k_few_rows(const PackedArgs a, const FewShape f) {
   using Values = Groups<FMT, NG>;
-  constexpr int kRows = 4 * VR;
   constexpr int kStepBytes = 2 * kStep;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int lane = lane_id(), n = lane & 15, q = lane >> 4;
@@ -278,7 +278,7 @@ void k_few_rows(const PackedArgs a, const FewShape f) {
   const int total = a.T * a.k;
 
   int e, p0, rows;
-  if (!find_run<kRows>(a.offsets, a.E, total, blockIdx.y, &e, &p0, &rows)) return;
+  if (!find_run(a.offsets, a.E, total, blockIdx.y, f.most, &e, &p0, &rows)) return;
   const int steps = (a.K + kStep - 1) / kStep;
   const int value_bytes = a.K / a.group * Values::kSize;  // of a row
   const int64_t all_values = static_cast<int64_t>(a.E) * a.N * value_bytes;
@@ -716,7 +716,7 @@ __global__ __launch_bounds__(64 * kMostWaves) void k_small(const PackedArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
   const int total = a.T * a.k, n0 = 16 * blockIdx.x;
   int e, p0, rows;
-  if (!find_run<kRows>(a.offsets, a.E, total, blockIdx.y, &e, &p0, &rows)) return;
+  if (!find_run(a.offsets, a.E, total, blockIdx.y, kRows, &e, &p0, &rows)) return;
   const int G = a.K / a.group, chunks = (a.K + kChunk - 1) / kChunk;
   const int64_t w_row = static_cast<int64_t>(e) * a.N + min(n0 + n, a.N - 1);
   const char* codes = reinterpret_cast<const char*>(a.codes) + w_row * (a.K / 2);
@@ -835,7 +835,7 @@ __global__ __launch_bounds__(256) void k_short_rows(const PackedArgs a) {
 //    rows k_small (7.5 us; k_few_rows 8.2, k_many_rows 13), from 5 on k_many_rows
 //    (13 rows of 2053 x 4000, groups of 32: 8.1 us; with all of x in registers as in
 //    k_small 9.0). Six experts with a row each (1536 tiles) 29 us with k_small and
-//    16 with k_few_rows.
+//    15 with k_few_rows.
 //  - Tiles of k_many_rows are as wide as leaves 192 workgroups (64 rows of 32768 x
 //    8192, groups of 128: 118 us; 143 with 400, 207 with 96).
 constexpr int64_t kFewRows = 20, kSmallTiles = 512, kEnoughGroups = 192;
@@ -848,10 +848,11 @@ hipError_t launch_short(const PackedArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Runs of up to `most` rows that the buckets can have together (find_run).
+// Runs of up to `most` rows that the buckets can have together (find_run), each of a
+// row at least.
 int64_t most_runs(const PackedArgs& a, int most) {
   const int64_t n = static_cast<int64_t>(a.T) * a.k;
-  return a.offsets ? std::min<int64_t>(n, a.E) + n / most : (n + most - 1) / most;
+  return a.offsets ? std::min(n, std::min<int64_t>(n, a.E) + n / most) : (n + most - 1) / most;
 }
 constexpr int64_t kMostY = 65535;
 
@@ -872,19 +873,24 @@ hipError_t allow_lds() {
 
 template <int TYPE, int FMT, int NG, int VR>
 hipError_t launch_few(const PackedArgs& a, hipStream_t s) {
-  constexpr int kRows = 4 * VR;
-  const int n = a.T * a.k, steps = (a.K + kStep - 1) / kStep, rows = std::min(kRows, n);
+  const int n = a.T * a.k, steps = (a.K + kStep - 1) / kStep;
+  // A token's experts are different ones as a rule, so a run need not hold more rows
+  // than there are tokens (or rows in the average bucket). The less of x there is in
+  // LDS, the more workgroups share a CU: top-6 experts of 4096 x 4096, 1 token 14.6
+  // us, 16.7 with runs of 8; 2 tokens 23 and 30, 4 tokens 46 and 52.
+  const int buckets = a.offsets ? std::min(n, a.E) : 1;
+  const int most = std::min(4 * VR, std::max(a.T, (n + buckets - 1) / buckets)), rows = std::min(most, n);
   const int64_t tiles = (a.N + 15) / 16;
-  const int64_t y = most_runs(a, kRows);
+  const int64_t y = most_runs(a, most);
   const int step_bytes = rows * (2 * kStep + (FMT == 0 ? kStepChunks * NG * 4 : 0));
   // LDS beside the steps of x
   auto fixed = [&](int waves, int kw) {
     return rows * kPad + waves * kValueLds<FMT> + (kw == 1 ? 0 : 2 * waves * rows * 16 * 4);
   };
   // Small workgroups, three to a CU, where x and the parts leave them the room
-  // (a token's six experts of 4096 x 4096: 16 us; 18 with one of 8 waves; four to a
-  // CU are no faster).
-  const int waves = fixed(4, 4) + steps * step_bytes <= kLds / 3 ? 4 : 8, per_cu = waves == 4 ? 3 : 1;
+  // (a token's six experts of 4096 x 4096: 14.6 us; 18 with one of 8 waves; four to
+  // a CU are no faster).
+  const int waves = fixed(4, 4) + steps * step_bytes <= kLds / 3 ? 4 : kMostWaves, per_cu = waves == 4 ? 3 : 1;
   // As few waves to a contraction as still give every wave a tile.
   int kw_log2 = 0;
   while ((2 << kw_log2) <= waves && (2 << kw_log2) <= steps && (tiles * y << kw_log2) < 256 * per_cu * waves &&
@@ -903,7 +909,7 @@ hipError_t launch_few(const PackedArgs& a, hipStream_t s) {
   auto launch = [&](hipError_t allowed, auto kernel) {
     if (allowed != hipSuccess) return allowed;
     QSMOE_LAUNCH(kernel, dim3(static_cast<unsigned>(gx), static_cast<unsigned>(y)), dim3(64 * waves), lds, s, a,
-                 FewShape{kw_log2, seg, own});
+                 FewShape{most, kw_log2, seg, own});
     return hipGetLastError();
   };
   // pieces start at multiples of 16 bytes too: of the steps of 8 bytes at even ones

@@ -200,6 +200,28 @@ def test_many_buckets(fmt, group, T, k, E, N, K, skew):
 
 
 @pytest.mark.parametrize("fmt,group", FORMATS)
+@pytest.mark.parametrize("T,k,E,N", [(1, 6, 8, 1500), (1, 40, 4, 3000), (2, 9, 5, 2100), (3, 5, 24, 800), (5, 7, 16, 600)])
+@pytest.mark.parametrize("one", [False, True])
+def test_buckets_longer_than_there_are_tokens(fmt, group, T, k, E, N, one):
+    """An expert named several times by one token, or by every assignment: more rows than a run is expected to hold."""
+    rng = np.random.default_rng(31 * T + k)
+    K = 640
+    ids = np.full(T * k, E // 2) if one else rng.integers(0, E, T * k)
+    off = np.r_[0, np.cumsum(np.bincount(ids, minlength=E))].astype(np.int32)
+    perm = np.argsort(ids, kind="stable").astype(np.int32)
+    x = torch.from_numpy(rng.standard_normal((T, K))).to(torch.bfloat16)
+    codes, s, b = weights(rng, (E, N), K, fmt, group)
+    y = qm.grouped_matmul_packed(x.cuda(), *on_device((codes, s, b)), dev(off), perm=dev(perm), top_k=k, x_order="token",
+                                 out=torch.full((T * k, N), float("nan"), device="cuda"))
+    assert torch.isfinite(y).all()
+    rows, at = oracle.source_rows(x.double().numpy(), "token", perm, k), sampled(N)
+    for e in np.unique(ids):
+        r = slice(off[e], off[e + 1])
+        want, mag = oracle.matmul_packed(rows[r], codes[e][at], s[e][at], None if b is None else b[e][at])
+        close(y[r][:, torch.from_numpy(at).cuda()], want, tolerance(mag, K, group), "f32")
+
+
+@pytest.mark.parametrize("fmt,group", FORMATS)
 def test_scales_behind_a_row_are_not_its_own(fmt, group):
     """Every second row's scales are no numbers: the rows between, whose blocks of scales reach into them, are as
     without."""
