@@ -840,10 +840,12 @@ __global__ __launch_bounds__(256) void k_short_rows(const PackedArgs a) {
 //    8192, groups of 128: 118 us; 143 with 400, 207 with 96).
 constexpr int64_t kFewRows = 20, kSmallTiles = 512, kEnoughGroups = 192;
 
+// The kernel steps on by grid.y: no more of it than a grid's threads leave room for.
 template <int TYPE, int FMT>
 hipError_t launch_short(const PackedArgs& a, hipStream_t s) {
-  const dim3 grid((a.N + 255) / 256, std::min(a.T * a.k, 65535));
-  if (static_cast<int64_t>(grid.x) * grid.y > max_workgroups(256)) return hipErrorInvalidValue;
+  const int columns = (a.N + 255) / 256;
+  const int64_t most_rows = std::min<int64_t>(65535, max_workgroups(256) / columns);
+  const dim3 grid(columns, static_cast<unsigned>(std::min<int64_t>(int64_t{a.T} * a.k, most_rows)));
   QSMOE_LAUNCH((k_short_rows<TYPE, FMT>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
