@@ -377,6 +377,7 @@ _I32 = (torch.int32,)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_forward_ad = torch.autograd.forward_ad  # _current_level: -1 outside of every dual level (0.03 us)
 
 
 def _operand(t: torch.Tensor, name: str, dtypes, dims, device=None) -> torch.Tensor:
@@ -389,12 +390,17 @@ def _operand(t: torch.Tensor, name: str, dtypes, dims, device=None) -> torch.Ten
     return t
 
 
-def _unrecorded(call: str) -> None:
-    """Refuse a product that autograd would have to record: its result would
-    look like a constant, and the operands' gradients would be lost in silence."""
-    if torch.is_grad_enabled():
+def _unrecorded(call: str, *operands: Optional[torch.Tensor]) -> None:
+    """Refuse a call that autograd would have to record: its result would look
+    like a constant, and the operands' gradients, or tangents in forward mode,
+    would be lost in silence."""
+    given = [t for t in operands if t is not None]
+    if torch.is_grad_enabled() and any(t.requires_grad for t in given):
         raise RuntimeError(f"{call} is not recorded by autograd, but an operand requires grad: call it under "
                            "torch.no_grad(), with detached operands, or inside a torch.autograd.Function")
+    if any(_forward_ad.unpack_dual(t).tangent is not None for t in given):
+        raise RuntimeError(f"{call} is not recorded by autograd, but an operand has a forward-mode tangent: call it "
+                           "with the operands' primals, or inside a torch.autograd.Function that has a jvp")
 
 
 def _shape(t: torch.Tensor, name: str, shape) -> None:
@@ -498,8 +504,9 @@ def matmul_block(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_sca
     instruction, which drops the low bits of small products next to large ones;
     `f32_sums` makes its sums fp32, as those of the other types always are.
     Not recorded by autograd: operands that require grad are refused."""
-    if a.requires_grad or a_scales.requires_grad or b.requires_grad or b_scales.requires_grad:
-        _unrecorded("matmul_block")
+    if (a.requires_grad or a_scales.requires_grad or b.requires_grad or b_scales.requires_grad
+            or _forward_ad._current_level >= 0):
+        _unrecorded("matmul_block", a, a_scales, b, b_scales)
     dev = _operand(a, "a", _FP8, (2,)).device
     M, K = a.shape
     N = _operand(b, "b", _FP8, (2,), dev).shape[0]
@@ -544,8 +551,9 @@ def grouped_matmul_block(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tenso
     and perm as `permute` gives them -> [T * top_k][N] in `out_order` ("bucket"
     or "slot"). Rows of no bucket are not written. `f32_sums` and operands that
     require grad as in matmul_block."""
-    if a.requires_grad or a_scales.requires_grad or w.requires_grad or w_scales.requires_grad:
-        _unrecorded("grouped_matmul_block")
+    if (a.requires_grad or a_scales.requires_grad or w.requires_grad or w_scales.requires_grad
+            or _forward_ad._current_level >= 0):
+        _unrecorded("grouped_matmul_block", a, a_scales, w, w_scales)
     dev = _operand(a, "a", _FP8, (2,)).device
     E, N, K = _operand(w, "w", _FP8, (3,), dev).shape
     rows = a.shape[0]
@@ -576,8 +584,8 @@ def grouped_matmul(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, perm
     says otherwise. Not recorded by autograd (operands that require grad are
     refused): the gradients are this call with `transposed` and
     grouped_matmul_dw."""
-    if x.requires_grad or w.requires_grad:
-        _unrecorded("grouped_matmul")
+    if x.requires_grad or w.requires_grad or _forward_ad._current_level >= 0:
+        _unrecorded("grouped_matmul", x, w)
     dev = _operand(x, "x", _B16, (2,)).device
     E, N, K = _operand(w, "w", (x.dtype,), (3,), dev).shape
     rows = x.shape[0]
@@ -603,8 +611,8 @@ def grouped_matmul_dw(x: torch.Tensor, dy: torch.Tensor, offsets: torch.Tensor, 
     x [rows][K] in `x_order`, dy [T * top_k][N] in `dy_order` ("bucket" or
     "slot") -> [E][N][K], the sum over each expert's positions of dy x^T. Not
     recorded by autograd either."""
-    if x.requires_grad or dy.requires_grad:
-        _unrecorded("grouped_matmul_dw")
+    if x.requires_grad or dy.requires_grad or _forward_ad._current_level >= 0:
+        _unrecorded("grouped_matmul_dw", x, dy)
     dev = _operand(x, "x", _B16, (2,)).device
     rows, K = x.shape
     N = _operand(dy, "dy", (x.dtype,), (2,), dev).shape[1]
@@ -671,8 +679,8 @@ def gather_rows(x: torch.Tensor, perm: torch.Tensor, top_k: int = 1, x_order: st
     (operands that require grad are refused): the gradient in x is combine_rows
     of the rows' gradient, the one in the weights combine_rows_grad's second
     result for (x, the rows' gradient, weights)."""
-    if x.requires_grad or (weights is not None and weights.requires_grad):
-        _unrecorded("gather_rows")
+    if x.requires_grad or (weights is not None and weights.requires_grad) or _forward_ad._current_level >= 0:
+        _unrecorded("gather_rows", x, weights)
     dev = _operand(x, "x", _DT, (2,)).device
     if x_order not in ("token", "slot"):
         raise ValueError(f"row order must be token or slot, got {x_order!r}")
@@ -718,8 +726,8 @@ def combine_rows(y: torch.Tensor, weights: Optional[torch.Tensor] = None, positi
     Not recorded by autograd (operands that require grad are refused): the
     gradients are combine_rows_grad's."""
     if y.requires_grad or (weights is not None and weights.requires_grad) or (
-            y_shared is not None and y_shared.requires_grad):
-        _unrecorded("combine_rows")
+            y_shared is not None and y_shared.requires_grad) or _forward_ad._current_level >= 0:
+        _unrecorded("combine_rows", y, weights, y_shared)
     dev = _operand(y, "y", _DT, (2,)).device
     n, d = y.shape
     T, top_k = _slots(n, positions, weights, top_k, dev)
@@ -743,8 +751,8 @@ def combine_rows_grad(dout: torch.Tensor, y: torch.Tensor, weights: torch.Tensor
     """The gradients of combine_rows (moe_combine_rows_grad): dout [T][d], y and
     weights as there -> (dy of y's shape and type, dweights fp32 [T][top_k]).
     Rows of dy that no position names are not written. `out` takes dy."""
-    if dout.requires_grad or y.requires_grad or weights.requires_grad:
-        _unrecorded("combine_rows_grad")
+    if dout.requires_grad or y.requires_grad or weights.requires_grad or _forward_ad._current_level >= 0:
+        _unrecorded("combine_rows_grad", dout, y, weights)
     dev = _operand(dout, "dout", _DT, (2,)).device
     n, d = _operand(y, "y", _DT, (2,), dev).shape
     T, top_k = _slots(n, positions, _operand(weights, "weights", _F32, (2,), dev), None, dev)
@@ -769,8 +777,8 @@ def swiglu(gu: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) ->
     """silu(gate) * up of gu [rows][gate | up] (moe_swiglu) -> [rows][inner] of
     gu's type. Not recorded by autograd (a gu that requires grad is refused): the
     gradient is swiglu_grad."""
-    if gu.requires_grad:
-        _unrecorded("swiglu")
+    if gu.requires_grad or _forward_ad._current_level >= 0:
+        _unrecorded("swiglu", gu)
     dev = _operand(gu, "gu", _DT, (2,)).device
     if _elsewhere(dev, stream):
         with _on(dev, stream):
@@ -790,8 +798,8 @@ def swiglu(gu: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) ->
 def swiglu_grad(gu: torch.Tensor, dh: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The gradient of swiglu (moe_swiglu_grad): gu [rows][gate | up], dh
     [rows][inner] -> dgu of gu's shape and type."""
-    if gu.requires_grad or dh.requires_grad:
-        _unrecorded("swiglu_grad")
+    if gu.requires_grad or dh.requires_grad or _forward_ad._current_level >= 0:
+        _unrecorded("swiglu_grad", gu, dh)
     dev = _operand(gu, "gu", _DT, (2,)).device
     rows, two = gu.shape
     if two % 2:
@@ -827,7 +835,8 @@ def _packed(codes: torch.Tensor, scales: torch.Tensor, biases: Optional[torch.Te
 
 
 def _grad_of_packed(x, scales, biases) -> bool:
-    return x.requires_grad or scales.requires_grad or (biases is not None and biases.requires_grad)
+    return (x.requires_grad or scales.requires_grad or (biases is not None and biases.requires_grad)
+            or _forward_ad._current_level >= 0)
 
 
 def matmul_packed(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, biases: Optional[torch.Tensor] = None,
@@ -839,7 +848,7 @@ def matmul_packed(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, bi
     says otherwise. For few rows. Not recorded by autograd: operands that require
     grad are refused."""
     if _grad_of_packed(x, scales, biases):
-        _unrecorded("matmul_packed")
+        _unrecorded("matmul_packed", x, scales, biases)
     dev = _operand(x, "x", _B16, (2,)).device
     M, K = x.shape
     N = _operand(codes, "codes", _I32, (2,), dev).shape[0]
@@ -864,7 +873,7 @@ def grouped_matmul_packed(x: torch.Tensor, codes: torch.Tensor, scales: torch.Te
     matmul_packed with E in front, orders, offsets and perm as in grouped_matmul ->
     [T * top_k][N] in `out_order`. Rows of no bucket are not written."""
     if _grad_of_packed(x, scales, biases):
-        _unrecorded("grouped_matmul_packed")
+        _unrecorded("grouped_matmul_packed", x, scales, biases)
     dev = _operand(x, "x", _B16, (2,)).device
     rows, K = x.shape
     E, N, _ = _operand(codes, "codes", _I32, (3,), dev).shape
