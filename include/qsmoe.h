@@ -529,17 +529,21 @@ moe_status moe_grouped_matmul_dw(const void* x, const void* dy, int32_t dtype, i
  * y_shared [T][d] of type dtype; topk_w NULL: ones; positions NULL: y is in
  * slot order, [T*k][d] (n == T*k). A position -1 adds nothing (y's row and its
  * weight are not read), one outside [-1, n) sets MOE_DEVERR_ROW_INDEX and adds
- * nothing. This is also the gradient of moe_gather_rows in x.
+ * nothing. This is also the gradient of moe_gather_rows in x, for a perm that
+ * names no assignment twice (moe_invert_perm keeps one position of each): in
+ * token order with its k, in slot order with k = 1.
  *
  * moe_combine_rows_grad: the gradient of moe_combine_rows in y and the weights:
  * dy[p] = topk_w[a] * dout[a / k] and dw[a] = sum over columns of dout[a / k] *
  * y[p], p = positions[a]. dout [T][d] of type dout_dtype, dy [n][d] of y's type
  * dtype, dw fp32 [T][k] (zero for a position -1). Rows of dy that no position
- * names are not written; where two assignments name one row, dy holds one of
- * their two gradients (moe_invert_perm gives no such positions). y_shared's
- * gradient is dout.
- * The gradient of moe_gather_rows in its weights is this call's dw with x in
- * the place of dout and the gathered rows' gradient in the place of y.
+ * names are not written. Where two assignments name one row, each element of
+ * dy's row is of either one's gradient, not their sum, and which one is not
+ * specified (moe_invert_perm gives no such positions); dw is as said.
+ * y_shared's gradient is dout.
+ * The gradient of moe_gather_rows (token order, no assignment named twice) in
+ * its weights is this call's dw with x in the place of dout and the gathered
+ * rows' gradient in the place of y.
  *
  * Nothing to write: MOE_OK without a launch (d == 0 still writes dw's zeros).
  * Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, HIP.

@@ -676,9 +676,10 @@ def gather_rows(x: torch.Tensor, perm: torch.Tensor, top_k: int = 1, x_order: st
     (`x_order` "token") or x[perm[p]] ("slot"), times weights[T][top_k] at
     perm[p] if given. Rows of entries -1 are not written. The output type is x's
     unless `out_dtype` or `out` says otherwise. Not recorded by autograd
-    (operands that require grad are refused): the gradient in x is combine_rows
-    of the rows' gradient, the one in the weights combine_rows_grad's second
-    result for (x, the rows' gradient, weights)."""
+    (operands that require grad are refused): with perm naming no assignment
+    twice, the gradient in x is combine_rows of the rows' gradient, the one in
+    the weights (token order) combine_rows_grad's second result for (x, the
+    rows' gradient, weights)."""
     if x.requires_grad or (weights is not None and weights.requires_grad) or _forward_ad._current_level >= 0:
         _unrecorded("gather_rows", x, weights)
     dev = _operand(x, "x", _DT, (2,)).device
@@ -750,7 +751,8 @@ def combine_rows_grad(dout: torch.Tensor, y: torch.Tensor, weights: torch.Tensor
                       err: Optional[torch.Tensor] = None, stream=None):
     """The gradients of combine_rows (moe_combine_rows_grad): dout [T][d], y and
     weights as there -> (dy of y's shape and type, dweights fp32 [T][top_k]).
-    Rows of dy that no position names are not written. `out` takes dy."""
+    Rows of dy that no position names are not written, one that several name is
+    not their sum. `out` takes dy."""
     if dout.requires_grad or y.requires_grad or weights.requires_grad or _forward_ad._current_level >= 0:
         _unrecorded("combine_rows_grad", dout, y, weights)
     dev = _operand(dout, "dout", _DT, (2,)).device
