@@ -455,8 +455,8 @@ moe_status moe_matmul_block(const uint8_t* a, const float* a_scales, const uint8
  * positions outside every bucket (before offsets[0], from offsets[E] on) are
  * neither read nor written, so their output rows stay as they were. Offsets
  * are clamped to [0, T*k], and a bucket that runs backwards counts as empty;
- * where buckets overlap for that reason, their common positions get the result
- * of one of them or none. A perm entry outside [0, T*k) sets
+ * where buckets overlap for that reason, their positions get the result of one
+ * of their buckets or none. A perm entry outside [0, T*k) sets
  * MOE_DEVERR_ROW_INDEX in *err (device int32 or NULL); some row of the matrix
  * is read in its place, and an output row that it would name is not written.
  * perm may be NULL when no matrix is in token or slot order; it must not name
@@ -581,8 +581,9 @@ moe_status moe_swiglu_grad(const void* gu, int32_t dtype, const void* dh, int32_
  * moe_grouped_matmul_packed: the same with codes [E][N][K / 8] and so on, rows
  * grouped by expert as in moe_grouped_matmul (positions outside every bucket,
  * clamped offsets and perm entries out of range as described there).
- * Meant for few rows of x for each matrix (tokens being decoded): each pass
- * over a matrix takes 4 to 64 rows. Products are exact, sums fp32: within a
+ * Meant for few rows of x for each matrix (tokens being decoded): a pass over a
+ * matrix takes up to 16 rows where there are few of them, 16 to 64 where there
+ * are more, and one with K below 128. Products are exact, sums fp32: within a
  * group sum x * code and sum x are formed first and multiplied by the scale
  * and added with the bias then, so a row of x with an infinity or a NaN (or one
  * of 2^117 and more) gives values that are not finite, and so does such a
@@ -590,8 +591,8 @@ moe_status moe_swiglu_grad(const void* gu, int32_t dtype, const void* dh, int32_
  * K % 32 == 0, K % group == 0, K >= 32, N any; N and K <= 2^20, M and T*k <=
  * 2^30, E <= 1024, k >= 1. x and codes 16-byte, scales, biases and out aligned
  * to their elements, offsets, perm and err to 4 bytes. M, T or N of 0: MOE_OK.
- * Errors: INVALID_ARG, UNSUPPORTED (sizes, format, group, fp32 x), ALIGNMENT,
- * HIP.
+ * Errors: INVALID_ARG, UNSUPPORTED (sizes as above, or an output of more tiles
+ * than a grid holds, 2^23; format, group, fp32 x), ALIGNMENT, HIP.
  */
 moe_status moe_matmul_packed(const void* x, int32_t dtype, const uint32_t* codes, const void* scales,
                            const uint16_t* biases, int32_t format, int32_t group, int32_t M, int32_t N, int32_t K,

@@ -15,10 +15,9 @@
 // chunk, 1.1 a code and lane, which the vector units do at twice the rate at
 // which HBM delivers codes.
 //
-// Three kernels: k_few_rows streams a matrix past up to 16 rows of x in LDS,
-// k_many_rows goes over it with tiles of 16 to 64 rows, k_small is for products
-// that end before a stream has begun. k_short_rows takes contractions shorter than
-// a chunk.
+// k_few_rows streams a matrix past up to 16 rows of x in LDS, k_many_rows goes over
+// it with tiles of 16 to 64 rows, k_small is for products that end before a stream
+// has begun. k_short_rows takes contractions shorter than a chunk.
 #include <algorithm>
 #include <atomic>
 
@@ -235,8 +234,8 @@ __device__ __forceinline__ void store_value(const PackedArgs& a, int row, int n,
 
 // Row r of x in a left operand of 4 VR rows, from its row m of 16, or -1. Element
 // v of lane (n, q) in the result is its row 4 q + v, which holds row 4 v + q of x:
-// up to 4 rows of x need one element a lane and one multiplication by each scale,
-// 8 two, 16 four.
+// up to 4 rows of x need one element a lane and one multiplication by each scale
+// (k_small), 8 two, 16 four (k_few_rows).
 template <int VR>
 __device__ __forceinline__ int x_row(int m) {
   return m % 4 < VR ? m % 4 * 4 + m / 4 : -1;
@@ -258,10 +257,14 @@ struct FewShape {
 // multiplying ones through the wave's own part of LDS.
 //
 // HBM bounds it: 129280 x 4096 with one row 57 to 65 us, 4.6 to 5.2 TB/s; 64
-// tokens' top-6 of 256 experts of 4096 x 4096 314 us, 5.4 TB/s of the experts
-// used; 512 tokens (12 rows a bucket, several runs where it is popular) 634. Loads
-// that bypass the caches are 2 to 6 % slower. A third wave to a SIMD is worth the
-// registers that it costs.
+// tokens' top-6 of 256 experts of 4096 x 4096 314 us, 5.4 TB/s of the experts that
+// are expected in use; 512 tokens (12 rows a bucket, several runs where it is
+// popular) 634. Loads that bypass the caches are 2 to 6 % slower. A third wave to a
+// SIMD is worth the registers that it costs, but only short rows of x leave room for
+// it: 3, 8 and 16 rows of 32768 x 8192 have two (the counters say so too) and take
+// 42, 48 and 55 us where one row takes 35. Buckets of 17 rows and more stream their
+// weights once per run of 16: about 18 rows of each of 64 experts of 4096 x 4096 212 to
+// 249 us, where 570 MB of weights are needed and 970 MB read.
 // WHOLE: a row's values and the steps at which a wave's blocks of them begin are
 // multiples of 16 bytes, so that none of the pieces ends behind its row.
 template <int TYPE, int FMT, int NG, int VR, bool WHOLE>
@@ -536,8 +539,13 @@ __device__ __forceinline__ Chunk<FMT, NG> load_chunk(const char* codes, const ch
 // as the matrix cores have the time. Loads stand outside of branches and values
 // are shifted to their places when used: with either one the other way round the
 // compiler waits for all loads of a stage (64 rows of 4096 x 4096: 26 us, now 19).
-// Unpacking and scaling bound it, 36 + 16 NG AB instructions per chunk against 4
-// (AB + 1) matrix products: 1024 rows of 4096 x 4096 70 us, 0.49 PFLOP/s.
+// A chunk is 36 + 16 NG AB vector instructions against 4 (AB + 1) matrix products
+// (1024 rows of 4096 x 4096 70 to 79 us, 0.43 to 0.49 PFLOP/s: matrix units busy 31 %
+// of the time). With 17 to 64 rows neither bounds it: 64 rows of 32768 x 8192, groups
+// of 128, 90 to 98 us, matrix units busy 24 %, vector instructions issued 45 %, and
+// the waves wait 36 % of their time. Two waves a SIMD are all that 136 KB of LDS and
+// up to 256 registers leave (AB 4, KW 4), and each stage ends in a barrier for eight
+// waves. 64 rows of 4096 x 4096: 128 workgroups, half of the CUs, 19 us.
 template <int TYPE, int FMT, int NG, int AB, int RT, int CH, int KW>
 __global__ __launch_bounds__(64 * kMostWaves) void k_many_rows(const PackedArgs a, const int ctiles, const int run) {
   constexpr int BM = 16 * AB, kw = KW, slots = KW * CH, subs = kMostWaves / KW;
@@ -777,7 +785,9 @@ __global__ __launch_bounds__(64 * kMostWaves) void k_small(const PackedArgs a) {
   }
 }
 
-// Contractions shorter than a chunk: a thread per result.
+// Contractions shorter than a chunk: a thread per result, which reads its row of W by
+// itself and computes without matrix products. One row of 129280 x 64 4.7 us, 64 rows
+// of 4096 x 64 7, 512 of 4096 x 96 43 (9.4 TFLOP/s).
 template <int TYPE, int FMT>
 __global__ __launch_bounds__(256) void k_short_rows(const PackedArgs a) {
   const int n = blockIdx.x * 256 + threadIdx.x, total = a.T * a.k, G = a.K / a.group;
@@ -830,14 +840,18 @@ __global__ __launch_bounds__(256) void k_short_rows(const PackedArgs a) {
 //  - Buckets of more than 20 rows on average go to k_many_rows. k_few_rows and
 //    k_many_rows: 18 rows of each of 64 experts (groups of 128) 212 and 251 us, 24
 //    rows 270 and 252; 18 rows of 16 experts of 2048 x 2048 33 and 39 us, 32 rows 51
-//    and 42; 512 tokens' top-6 of 256 experts (12 rows) 634 and 1200.
+//    and 42; 512 tokens' top-6 of 256 experts (12 rows) 634 and 1200. Dense products
+//    take the same border, though 17 to 20 of their rows are two runs, which stream
+//    the matrix twice: 18 rows of 16384 x 2048 (groups of 32) 19.4 us, 24 rows 15.5;
+//    of 32768 x 4096 38 and 42.
 //  - Up to 512 tiles of 16 rows of W, all buckets together, are no stream: up to 4
 //    rows k_small (7.5 us; k_few_rows 8.2, k_many_rows 13), from 5 on k_many_rows
 //    (13 rows of 2053 x 4000, groups of 32: 8.1 us; with all of x in registers as in
 //    k_small 9.0). Six experts with a row each (1536 tiles) 29 us with k_small and
 //    15 with k_few_rows.
 //  - Tiles of k_many_rows are as wide as leaves 192 workgroups (64 rows of 32768 x
-//    8192, groups of 128: 118 us; 143 with 400, 207 with 96).
+//    8192, groups of 128: 118 us when it was chosen, 143 with 400, 207 with 96; 90 to
+//    98 now).
 constexpr int64_t kFewRows = 20, kSmallTiles = 512, kEnoughGroups = 192;
 
 // The kernel steps on by grid.y: no more of it than a grid's threads leave room for.
@@ -951,8 +965,9 @@ hipError_t launch_many(const PackedArgs& a, hipStream_t s) {
 // CUs a workgroup.
 template <int TYPE, int FMT, int NG, int AB>
 hipError_t pick_many(const PackedArgs& a, int64_t rtiles, hipStream_t s) {
-  constexpr int kMost = AB == 4 && NG == 4 ? 1 : 2;  // as many tiles a wave as registers hold
-  constexpr int CH = AB == 1 ? 2 : 1;                // and chunks a stage
+  // Tiles a wave and chunks a stage: what registers hold, but for groups of 64 with
+  // AB 4 and KW 4, which take all 256 and spill 7.
+  constexpr int kMost = AB == 4 && NG == 4 ? 1 : 2, CH = AB == 1 ? 2 : 1;
   auto enough = [&](int columns) { return rtiles * ((a.N + columns - 1) / columns) >= kEnoughGroups; };
   if (enough(128 * kMost)) return launch_many<TYPE, FMT, NG, AB, kMost, CH, 1>(a, s);
   if (enough(32 * kMost)) return launch_many<TYPE, FMT, NG, AB, kMost, CH, 4>(a, s);

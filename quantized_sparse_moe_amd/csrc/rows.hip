@@ -12,7 +12,7 @@
 // atomics on values. Memory bounds them; a copy of 1 GiB runs at 5.1 TB/s read plus
 // written. 4096 tokens, top-6, rows of 4096 in bf16: gather 35 us (6.7 TB/s of what
 // it must move), combine 42 us in slot order and 47 in bucket order (5.6 and 5.0),
-// the gradient 85 us (5.1).
+// the gradient 85 to 88 us (5.1 to 5.0).
 #include <algorithm>
 
 #include "elements.hpp"
@@ -114,8 +114,12 @@ __global__ __launch_bounds__(256) void k_gather(const GatherArgs g, const RowSpl
 // Workgroup b runs on XCD b % 8: each XCD takes slices of 2^shift lanes' columns
 // one after the other, all rows of a slice together, so that a slice of x (2 MB of
 // 4096 rows) stays in its L2, and writes past the caches. 4096 tokens, top-6, rows
-// of 4096: 36 us with slices of 32 lanes, 38 with 16, 39 with 64; 61 row by row, 53
-// with the writes past the caches alone.
+// of 4096: 36 us with slices of 32 lanes, 38 with 16, 39 with 64; 61 to 69 row by row,
+// 53 with the writes past the caches alone. Where the slices are no multiple of 8, the
+// last ones occupy some of the XCDs only: 2304 columns (9 slices) 33 us, row by row 45;
+// 2048 20 and 30, 2560 34 and 48, 2880 36 and 54, 5120 53 and 91. Rows that are read
+// once gain the writes only: slot order 74 us, row by row 78, top-1 72 and 78. Slices
+// that no L2 holds (16384 tokens) 233, row by row 282.
 template <int IN, int OUT, bool WEIGHTED>
 __global__ __launch_bounds__(256) void k_gather_slices(const GatherArgs g, const int shift, const int slices,
                                                        const int per_slice) {
@@ -261,7 +265,8 @@ hipError_t launch_gather_rows(const GatherArgs& g, hipStream_t s) {
     return with_type(g.out_dtype, [&](auto out) {
       constexpr int IN = decltype(in)::value, OUT = decltype(out)::value, V = kLaneElems<IN, OUT>;
       // Slices for every XCD, a result larger than the eight L2s of 4 MB (smaller ones
-      // are the next kernel's to find there), and a grid that holds them.
+      // are the next kernel's to find there), and a grid that holds them. Every order,
+      // top_k and width measured above gains by it, so the rule asks for none.
       constexpr int shift = 5;
       const int slices = (g.d + (V << shift) - 1) / (V << shift);
       const int per_slice = (g.n + (256 >> shift) - 1) / (256 >> shift);
