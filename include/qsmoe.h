@@ -586,8 +586,9 @@ moe_status moe_swiglu_grad(const void* gu, int32_t dtype, const void* dh, int32_
  * are more, and one with K below 128. Products are exact, sums fp32: within a
  * group sum x * code and sum x are formed first and multiplied by the scale
  * and added with the bias then, so a row of x with an infinity or a NaN (or one
- * of 2^117 and more) gives values that are not finite, and so does such a
- * scale or bias; other rows are not affected. One rounding to out_dtype.
+ * of 2^117 and more, of less with scales above 1 or biases above 16) gives
+ * values that are not finite, and so does such a scale or bias; other rows are
+ * not affected. One rounding to out_dtype.
  * K % 32 == 0, K % group == 0, K >= 32, N any; N and K <= 2^20, M and T*k <=
  * 2^30, E <= 1024, k >= 1. x and codes 16-byte, scales, biases and out aligned
  * to their elements, offsets, perm and err to 4 bytes. M, T or N of 0: MOE_OK.
