@@ -377,7 +377,7 @@ _I32 = (torch.int32,)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-_forward_ad = torch.autograd.forward_ad  # _current_level: -1 outside of every dual level (0.03 us)
+_forward_ad = torch.autograd.forward_ad  # _current_level: -1 outside of every dual level (0.06 us)
 
 
 def _operand(t: torch.Tensor, name: str, dtypes, dims, device=None) -> torch.Tensor:
